@@ -281,9 +281,10 @@ def _plain_select(s):
         first = torch.arange(beams, device=x.device) == 0
         score = torch.where(f, torch.where(first, s["scores"].double()[..., None], -math.inf), score)
         token = torch.where(f, s["eos"], token)
-    score, at = torch.sort(score.reshape(b, -1), dim=1, descending=True, stable=True)
+    # compared as they are returned; equal ones: the lower beam, then the larger logit
+    score, at = torch.sort(score.float().reshape(b, -1), dim=1, descending=True, stable=True)
     score, at = score[:, :beams], at[:, :beams]
-    return {"scores": score.float(), "tokens": token.reshape(b, -1).gather(1, at).int(), "parents": (at // beams).int()}
+    return {"scores": score, "tokens": token.reshape(b, -1).gather(1, at).int(), "parents": (at // beams).int()}
 
 
 def _plain_reorder(s):
@@ -432,9 +433,11 @@ def _exact_select(case, s):
             if s["finished"] is not None and bool(s["finished"][b, i]):
                 total[i] = -math.inf
                 total[i, s["eos"]] = float(s["scores"][b, i])
-        flat = total.reshape(-1)
-        at = np.flatnonzero(flat >= np.partition(flat, flat.size - beams)[flat.size - beams])
-        at = at[np.lexsort((at, -flat[at]))][:beams]
+        flat, rounded = total.reshape(-1), total.reshape(-1).astype(np.float32)
+        at = np.flatnonzero(rounded >= np.partition(rounded, flat.size - beams)[flat.size - beams])
+        # equal as they are returned: the lower beam, then the larger logit, then the lower token
+        logit = s["logits"][b].reshape(-1)[torch.from_numpy(at).cuda()].double().cpu().numpy()
+        at = at[np.lexsort((at, -logit, at // case["vocab"], -rounded[at]))][:beams]
         scores.append(flat[at])
         tokens.append(at % case["vocab"])
         parents.append(at // case["vocab"])
