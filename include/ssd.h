@@ -28,7 +28,7 @@
  *    and are returned to the driver when the process exits.
  *  - The return value is an ssd_status.  On any host-detected error nothing is
  *    launched and no output is written.  Errors found on the device (bad
- *    cu_seqlens values, a bounded wait that ran out) are recorded in a per-device
+ *    cu_seqlens values or parents, a bounded wait that ran out) are recorded in a per-device
  *    status word, read with ssd_query_status().  With SSD_DEBUG set in the
  *    environment, a failed tensor-core launch also prints its CUDA error to stderr.
  */
@@ -55,8 +55,9 @@ typedef enum {
   SSD_ERR_CUDA = 4,           /* a CUDA runtime call or kernel launch failed                 */
   SSD_ERR_DEVICE_TIMEOUT = 5, /* a bounded device-side wait gave up (kernel returned early)  */
   SSD_ERR_BAD_SEQLENS = 6,    /* cu_seqlens not 0 = c0 <= c1 <= ... <= c_nseq = seqlen        */
-  SSD_ERR_SCRATCH_LIMIT = 7   /* ssd_forward_noalloc: the shape needs more scratch than
+  SSD_ERR_SCRATCH_LIMIT = 7,  /* ssd_forward_noalloc: the shape needs more scratch than
                                  SSD_NOALLOC_SCRATCH_BYTES                                   */
+  SSD_ERR_BAD_PARENT = 8      /* ssd_state_reorder: a parent outside 0 .. beams - 1          */
 } ssd_status;
 
 /*
@@ -249,13 +250,105 @@ int ssd_segment_logdecay(int64_t tokens, int64_t nheads, const float* dt, const 
 int ssd_state_prefix(int rank, int64_t nheads, int64_t headdim, int64_t dstate, const float* states,
                      const float* logdecay, const float* init_state, float* out, ssd_stream_t stream);
 
+/*
+ * Linear attention with a decay for each head.  For every sequence and head h (group
+ * g = h / (H/G)), with a P x N fp32 state S (as ssd_forward's) and a_t = exp(log_decay_t):
+ *     S_t = a_t S_{t-1} + v_t k_t^T,      y_t = scale * S_t q_t
+ * It is ssd_forward's recurrence without the step size: the decay does not scale the input,
+ * heads may have a query and key of their own (G = H), and there are gradients.
+ *
+ *   shape       nheads H, headdim P (of v and y), dstate N (of q and k), ngroups G; P and N
+ *               1..128, H % G == 0 (SSD_ERR_UNSUPPORTED otherwise); batch, seqlen, nseq,
+ *               io_dtype and cu_seqlens_host as for ssd_forward
+ *   q, k        (batch, seqlen, G, N)  io_dtype
+ *   v, y        (batch, seqlen, H, P)  io_dtype
+ *   log_decay   (batch, seqlen, H) fp32 with decay_per_token != 0, else (H): one constant for
+ *               each head.  Meant to be <= 0; -infinity is a decay of zero (the state before
+ *               that token is forgotten), and below -103.9 counts as -infinity
+ *   scale       a factor on y (1/sqrt(N) is usual)
+ *   init_state, final_state, cu_seqlens  as for ssd_forward, final_state optional
+ * Values that are not finite spoil their own sequence and head only, from the start of their
+ * block of 128 tokens (in the gradients: also everything before it).
+ * Sums, states and decays are held in 32 bits or more; bf16 outputs are rounded once, after
+ * products whose decayed factors are rounded to bf16 once.
+ */
+int ssd_linear_attention_forward(const ssd_shape* shape, const void* q, const void* k, const void* v,
+                                 const float* log_decay, int decay_per_token, float scale, const float* init_state,
+                                 const int32_t* cu_seqlens, void* y, float* final_state, ssd_stream_t stream);
+
+/*
+ * Gradients of ssd_linear_attention_forward: of a loss with gradient dy for y and (optional)
+ * dfinal_state for final_state.  Nothing of the forward pass is kept or needed but its inputs.
+ *   dy            (batch, seqlen, H, P)        io_dtype
+ *   dfinal_state  (nseq_or_batch, H, P, N)     fp32, or NULL (= 0)
+ *   dq, dk        (batch, seqlen, G, N)        io_dtype: summed over the heads that share them
+ *   dv            (batch, seqlen, H, P)        io_dtype
+ *   dlog_decay    log_decay's layout           fp32, or NULL (not computed, which is cheaper);
+ *                 constants: summed over all tokens; 0 where the decay is zero
+ *   dinit_state   (nseq_or_batch, H, P, N)     fp32, or NULL
+ * No output may alias an input.  Results do not depend on scheduling (no atomics).
+ */
+int ssd_linear_attention_backward(const ssd_shape* shape, const void* dy, const void* q, const void* k, const void* v,
+                                  const float* log_decay, int decay_per_token, float scale, const float* init_state,
+                                  const float* dfinal_state, const int32_t* cu_seqlens, void* dq, void* dk, void* dv,
+                                  float* dlog_decay, float* dinit_state, ssd_stream_t stream);
+
+/*
+ * One generation step of ssd_linear_attention_forward for a batch of rows (as
+ * ssd_decode_step): the state is read, advanced by one token and overwritten.
+ *   shape       batch = rows, seqlen = 1; the other sizes as above
+ *   q, k        (batch, G, N);  v, y  (batch, H, P)   io_dtype
+ *   log_decay   (batch, H) fp32 with decay_per_row != 0, else (H)
+ *   state       (batch, H, P, N) fp32
+ * No scratch.
+ */
+int ssd_linear_attention_step(const ssd_shape* shape, const void* q, const void* k, const void* v,
+                              const float* log_decay, int decay_per_row, float scale, float* state, void* y,
+                              ssd_stream_t stream);
+
+/*
+ * ssd_beam_select -- one selection step of beam search: the best `count` continuations of
+ * every batch item over its beams and the vocabulary.  Beam i continued by token w scores
+ *     scores[b,i] + logits[b,i,w] - log sum_w' exp(logits[b,i,w'])
+ * formed in 64 bits and compared in fp32, as it is returned; equal scores go to the lower beam,
+ * then the larger logit, then the lower token.  A finished beam has one continuation: `eos`,
+ * with its score unchanged.
+ *   logits       (batch, beams, vocab)  io_dtype; -infinity bans a token
+ *   scores       (batch, beams) fp32 cumulative log-probabilities (-infinity: an unused beam)
+ *   finished     (batch, beams) one byte each, or NULL (none is finished); needs 0 <= eos < vocab
+ *   out_scores   (batch, count) fp32, best first;  out_tokens, out_parents (batch, count) int32
+ * A score that is -infinity or not a number (a row with a NaN or +infinity logit) is no
+ * continuation.  Where fewer than `count` are left, the last entries are score -infinity,
+ * token eos (0 if negative) and their own place modulo `beams` as parent.
+ * beams and count 1..64, vocab 1..2^20.  Outputs may not alias inputs.  Two kernels; a few
+ * words of pool scratch per row.
+ */
+int ssd_beam_select(int64_t batch, int64_t beams, int64_t vocab, ssd_dtype logits_dtype, const void* logits,
+                    const float* scores, const uint8_t* finished, int32_t eos, int64_t count, float* out_scores,
+                    int32_t* out_tokens, int32_t* out_parents, ssd_stream_t stream);
+
+/*
+ * ssd_state_reorder -- after a beam search's selection: buffer row (b, i) <- row
+ * (b, parents[b,i]), in place, for every buffer at once (the recurrent states and convolution
+ * windows of all layers).  Rows whose parent is themselves are not touched.
+ *   parents    (batch, beams) int32 on the device, any mapping (not only permutations).  A
+ *              value outside 0..beams-1 leaves its row as it is and is recorded in the status
+ *              word (SSD_ERR_BAD_PARENT)
+ *   buffers    HOST array of nbuf device pointers, each (batch * beams) contiguous rows ...
+ *   row_bytes  HOST array: ... of this many bytes (any, 0 allowed)
+ * beams 1..64.  Buffers may not overlap (SSD_ERR_INVALID_ARG).  One kernel for up to 128
+ * buffers of 16-byte rows; no scratch.  Both arrays are read before the call returns.
+ */
+int ssd_state_reorder(int64_t batch, int64_t beams, const int32_t* parents, int64_t nbuf, void* const* buffers,
+                      const int64_t* row_bytes, ssd_stream_t stream);
+
 /* Bytes of stream-ordered scratch ssd_forward takes for this shape (informational). */
 size_t ssd_workspace_bytes(const ssd_shape* shape, int chunk);
 
 /*
  * Synchronises `stream`, then returns and clears the current device's status word:
- * SSD_OK, SSD_ERR_BAD_SEQLENS or SSD_ERR_DEVICE_TIMEOUT (SSD_ERR_CUDA if the
- * synchronisation itself failed).
+ * SSD_OK, SSD_ERR_BAD_SEQLENS, SSD_ERR_DEVICE_TIMEOUT or SSD_ERR_BAD_PARENT
+ * (SSD_ERR_CUDA if the synchronisation itself failed).
  */
 int ssd_query_status(ssd_stream_t stream);
 

@@ -11,7 +11,11 @@ buffers, copies pipelined with the compute), ``ssd_forward_noalloc`` (no device
 allocation), ``ssd_forward_dt`` (step size from the raw projection inside the
 kernels), ``ssd_decode_step`` (one generation step), ``causal_conv1d_silu`` and
 ``gated_rmsnorm`` (the block's steps around the SSD), ``segment_logdecay`` and
-``state_prefix`` (sequence parallelism, see ``sequence_parallel``).
+``state_prefix`` (sequence parallelism, see ``sequence_parallel``),
+``linear_attention_forward``, ``linear_attention_backward`` and
+``linear_attention_step`` (linear attention with a decay for each head: prompts,
+gradients, one generation step), ``beam_select`` and ``state_reorder`` (a beam
+search's selection, and its recurrent states brought in line).
 """
 from __future__ import annotations
 
@@ -35,6 +39,7 @@ STATUS = {
     5: "SSD_ERR_DEVICE_TIMEOUT",
     6: "SSD_ERR_BAD_SEQLENS",
     7: "SSD_ERR_SCRATCH_LIMIT",
+    8: "SSD_ERR_BAD_PARENT",
 }
 # Size of the static scratch array behind ssd_forward_noalloc (SSD_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -57,6 +62,11 @@ EXPORTS = (
     "ssd_segment_logdecay",
     "ssd_state_prefix",
     "ssd_set_test_hooks",
+    "ssd_linear_attention_forward",
+    "ssd_linear_attention_backward",
+    "ssd_linear_attention_step",
+    "ssd_beam_select",
+    "ssd_state_reorder",
 )
 
 
@@ -127,6 +137,17 @@ def _open() -> ctypes.CDLL:
     lib.ssd_state_prefix.restype = I
     lib.ssd_set_test_hooks.argtypes = [L, I]
     lib.ssd_set_test_hooks.restype = I
+    F = ctypes.c_float
+    lib.ssd_linear_attention_forward.argtypes = [SP, V, V, V, V, I, F, V, V, V, V, V]
+    lib.ssd_linear_attention_forward.restype = I
+    lib.ssd_linear_attention_backward.argtypes = [SP, V, V, V, V, V, I, F, V, V, V, V, V, V, V, V, V]
+    lib.ssd_linear_attention_backward.restype = I
+    lib.ssd_linear_attention_step.argtypes = [SP, V, V, V, V, I, F, V, V, V]
+    lib.ssd_linear_attention_step.restype = I
+    lib.ssd_beam_select.argtypes = [L, L, L, I, V, V, V, ctypes.c_int32, L, V, V, V, V]
+    lib.ssd_beam_select.restype = I
+    lib.ssd_state_reorder.argtypes = [L, L, V, L, V, V, V]
+    lib.ssd_state_reorder.restype = I
     return lib
 
 
@@ -445,6 +466,191 @@ def ssd_decode_step(x, dt, A, B, C, D, state, y: Optional[torch.Tensor] = None, 
     if rc:
         raise SsdError(rc, "ssd_decode_step")
     return y
+
+
+def _handle(stream, device):
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _attention_shape(q, k, v, log_decay, cu_seqlens, cu_seqlens_host):
+    """Checks what every linear attention call shares; returns (ssd_shape, rows, decay_per_token)."""
+    device = v.device
+    if device.type != "cuda":
+        raise ValueError("linear attention takes CUDA tensors")
+    if v.dim() not in (3, 4) or q.dim() != v.dim():
+        raise ValueError("q, k must be (batch, seqlen, G, N) and v (batch, seqlen, H, P); a step has no seqlen")
+    lead = tuple(v.shape[:-2])
+    H, P = v.shape[-2:]
+    G, N = q.shape[-2:]
+    _check("v", v, device)
+    _check("q", q, device, v.dtype, lead + (G, N))
+    _check("k", k, device, v.dtype, lead + (G, N))
+    per_token = log_decay.dim() != 1
+    _check("log_decay", log_decay, device, torch.float32, lead + (H,) if per_token else (H,))
+    _check("cu_seqlens", cu_seqlens, device, torch.int32)
+    if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2):
+        raise ValueError("cu_seqlens must hold nseq + 1 offsets")
+    nseq = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    T = v.shape[1] if v.dim() == 4 else 1
+    shape = SsdShape(v.shape[0], T, H, P, N, G, nseq, _io_code(v.dtype), None)
+    if cu_seqlens_host is not None:
+        if cu_seqlens is None or cu_seqlens_host.dtype != torch.int32 or cu_seqlens_host.numel() != nseq + 1:
+            raise ValueError("cu_seqlens_host must be an int32 host copy of cu_seqlens")
+        _check("cu_seqlens_host", cu_seqlens_host, torch.device("cpu"))
+        shape.cu_seqlens_host = ctypes.c_void_p(cu_seqlens_host.data_ptr())
+    return shape, nseq if cu_seqlens is not None else v.shape[0], per_token
+
+
+def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                             scale: Optional[float] = None, init_state: Optional[torch.Tensor] = None,
+                             cu_seqlens: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                             final_state: Optional[torch.Tensor] = None, return_final: bool = True, stream=None,
+                             cu_seqlens_host: Optional[torch.Tensor] = None
+                             ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay for each head: S_t = exp(log_decay_t) S_{t-1} + v_t k_t^T,
+    y_t = scale S_t q_t (see ``ssd_linear_attention_forward`` in include/ssd.h).
+
+    q, k (batch, T, G, N) and v (batch, T, H, P) fp32/bf16, H % G == 0, N and P up to 128;
+    log_decay (batch, T, H) or one constant per head (H,), fp32; scale: 1/sqrt(N) by default;
+    init_state (rows, H, P, N) fp32 or None; cu_seqlens (nseq+1,) int32 (packed batch,
+    batch == 1) or None.  Returns (y, final_state).  Asynchronous on ``stream`` (default:
+    torch's current stream).
+    """
+    shape, rows, per_token = _attention_shape(q, k, v, log_decay, cu_seqlens, cu_seqlens_host)
+    if v.dim() != 4:
+        raise ValueError("v must be (batch, seqlen, H, P)")
+    device, states = v.device, (rows, shape.nheads, shape.headdim, shape.dstate)
+    _check("init_state", init_state, device, torch.float32, states)
+    if y is None:
+        y = torch.empty_like(v)
+    _check("y", y, device, v.dtype, tuple(v.shape))
+    if final_state is None and return_final:
+        final_state = torch.empty(states, dtype=torch.float32, device=device)
+    _check("final_state", final_state, device, torch.float32, states)
+    scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
+    with torch.cuda.device(device):
+        rc = _lib.ssd_linear_attention_forward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                               int(per_token), scale, _ptr(init_state), _ptr(cu_seqlens), _ptr(y),
+                                               _ptr(final_state), _handle(stream, device))
+    if rc:
+        raise SsdError(rc, "ssd_linear_attention_forward")
+    return y, final_state
+
+
+def linear_attention_backward(dy: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              log_decay: torch.Tensor, scale: Optional[float] = None,
+                              init_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                              cu_seqlens: Optional[torch.Tensor] = None, need_dlog_decay: bool = True, stream=None,
+                              cu_seqlens_host: Optional[torch.Tensor] = None):
+    """Gradients of ``linear_attention_forward`` from those of its outputs: dy (batch, T, H, P)
+    and dfinal_state (rows, H, P, N) fp32 or None (see ``ssd_linear_attention_backward``).
+
+    Returns (dq, dk, dv, dlog_decay, dinit_state) in the inputs' types and layouts; dlog_decay
+    is None with need_dlog_decay=False (cheaper), dinit_state is None without init_state.
+    """
+    shape, rows, per_token = _attention_shape(q, k, v, log_decay, cu_seqlens, cu_seqlens_host)
+    if v.dim() != 4:
+        raise ValueError("v must be (batch, seqlen, H, P)")
+    device, states = v.device, (rows, shape.nheads, shape.headdim, shape.dstate)
+    _check("dy", dy, device, v.dtype, tuple(v.shape))
+    _check("init_state", init_state, device, torch.float32, states)
+    _check("dfinal_state", dfinal_state, device, torch.float32, states)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dlog = torch.empty_like(log_decay) if need_dlog_decay else None
+    dinit = torch.empty(states, dtype=torch.float32, device=device) if init_state is not None else None
+    scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
+    with torch.cuda.device(device):
+        rc = _lib.ssd_linear_attention_backward(ctypes.byref(shape), _ptr(dy), _ptr(q), _ptr(k), _ptr(v),
+                                                _ptr(log_decay), int(per_token), scale, _ptr(init_state),
+                                                _ptr(dfinal_state), _ptr(cu_seqlens), _ptr(dq), _ptr(dk), _ptr(dv),
+                                                _ptr(dlog), _ptr(dinit), _handle(stream, device))
+    if rc:
+        raise SsdError(rc, "ssd_linear_attention_backward")
+    return dq, dk, dv, dlog, dinit
+
+
+def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                          state: torch.Tensor, scale: Optional[float] = None, y: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """One generation step of ``linear_attention_forward`` for a batch of rows, state updated in
+    place: q, k (rows, G, N), v (rows, H, P), log_decay (rows, H) or (H,), state (rows, H, P, N)
+    fp32.  Returns y (rows, H, P)."""
+    shape, rows, per_row = _attention_shape(q, k, v, log_decay, None, None)
+    if v.dim() != 3:
+        raise ValueError("v must be (rows, H, P)")
+    device = v.device
+    _check("state", state, device, torch.float32, (rows, shape.nheads, shape.headdim, shape.dstate))
+    if y is None:
+        y = torch.empty_like(v)
+    _check("y", y, device, v.dtype, tuple(v.shape))
+    scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
+    with torch.cuda.device(device):
+        rc = _lib.ssd_linear_attention_step(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                            int(per_row), scale, _ptr(state), _ptr(y), _handle(stream, device))
+    if rc:
+        raise SsdError(rc, "ssd_linear_attention_step")
+    return y
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[torch.Tensor] = None, eos: int = -1,
+                count: Optional[int] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The best ``count`` (default: beams) continuations of every batch item over its beams and the
+    vocabulary, by scores + log_softmax(logits) as fp32; equal ones: the lower beam, larger logit, lower token.
+
+    logits (batch, beams, vocab) fp32/bf16; scores (batch, beams) fp32; finished (batch, beams)
+    bool or None: such a beam goes on by ``eos`` alone, its score unchanged.  Returns (scores
+    (batch, count) fp32 best first, tokens, parents (batch, count) int32); see ``ssd_beam_select``.
+    """
+    device = logits.device
+    if device.type != "cuda":
+        raise ValueError("beam_select takes CUDA tensors")
+    if logits.dim() != 3:
+        raise ValueError("logits must be (batch, beams, vocab)")
+    batch, beams, vocab = logits.shape
+    _check("logits", logits, device)
+    _check("scores", scores, device, torch.float32, (batch, beams))
+    _check("finished", finished, device, torch.bool, (batch, beams))
+    count = beams if count is None else int(count)
+    out = torch.empty((batch, count), dtype=torch.float32, device=device)
+    tokens, parents = (torch.empty((batch, count), dtype=torch.int32, device=device) for _ in range(2))
+    with torch.cuda.device(device):
+        rc = _lib.ssd_beam_select(batch, beams, vocab, _io_code(logits.dtype), _ptr(logits), _ptr(scores),
+                                  _ptr(finished), int(eos), count, _ptr(out), _ptr(tokens), _ptr(parents),
+                                  _handle(stream, device))
+    if rc:
+        raise SsdError(rc, "ssd_beam_select")
+    return out, tokens, parents
+
+
+def state_reorder(states, parents: torch.Tensor, stream=None) -> None:
+    """Row (b, i) of every state takes what row (b, parents[b, i]) held, in place.
+
+    states: tensors of any dtype with a leading dimension of batch * beams (recurrent states,
+    convolution windows, of all layers), contiguous and not overlapping; parents (batch, beams)
+    int32.  A parent outside 0 .. beams - 1 leaves its row and sets the status word
+    (``query_status``: SSD_ERR_BAD_PARENT)."""
+    device = parents.device
+    if device.type != "cuda":
+        raise ValueError("state_reorder takes CUDA tensors")
+    if parents.dim() != 2:
+        raise ValueError("parents must be (batch, beams)")
+    _check("parents", parents, device, torch.int32)
+    batch, beams = parents.shape
+    states = [states] if isinstance(states, torch.Tensor) else list(states)
+    for i, s in enumerate(states):
+        _check(f"states[{i}]", s, device)
+        if s.dim() < 1 or s.shape[0] != batch * beams:
+            raise ValueError(f"states[{i}] has shape {tuple(s.shape)}, expected {batch * beams} rows")
+    n = len(states)
+    rows = max(1, batch * beams)
+    ptrs = (ctypes.c_void_p * max(1, n))(*[s.data_ptr() for s in states])
+    sizes = (ctypes.c_int64 * max(1, n))(*[s.numel() // rows * s.element_size() for s in states])
+    with torch.cuda.device(device):
+        rc = _lib.ssd_state_reorder(batch, beams, _ptr(parents), n, ptrs, sizes, _handle(stream, device))
+    if rc:
+        raise SsdError(rc, "ssd_state_reorder")
 
 
 def ssd_forward_host(x, dt, A, B, C, D=None, init_state=None, cu_seqlens=None, chunk: int = 256, y=None,

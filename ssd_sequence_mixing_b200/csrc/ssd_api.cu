@@ -364,6 +364,8 @@ int forward_impl(const ssd_shape* s, const void* x, const float* dt, const float
 namespace ssd {
 void count_launches(int n) { g_launches.fetch_add((uint64_t)n); }
 unsigned int* device_status_word() { return status_ptr(); }
+cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t st) { return pool_alloc(ptr, bytes, st); }
+int device_sm_count() { return device_sms(); }
 int check_shape(const ssd_shape* s, bool packed, int chunk) {
   const void* f = (const void*)16;  // stands for every required pointer: only shapes are checked
   return validate(s, f, (const float*)f, (const float*)f, f, f, packed ? (const int32_t*)f : nullptr, chunk, f);
@@ -573,6 +575,7 @@ int ssd_query_status(ssd_stream_t stream) {
   }
   if (v & ssd::kStatusBadSeqlens) return SSD_ERR_BAD_SEQLENS;
   if (v & ssd::kStatusTimeout) return SSD_ERR_DEVICE_TIMEOUT;
+  if (v & ssd::kStatusBadParent) return SSD_ERR_BAD_PARENT;
   return SSD_OK;
 }
 
@@ -586,6 +589,7 @@ const char* ssd_status_string(int status) {
     case SSD_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait gave up";
     case SSD_ERR_BAD_SEQLENS: return "cu_seqlens must be 0 = c0 <= c1 <= ... <= c_nseq = seqlen";
     case SSD_ERR_SCRATCH_LIMIT: return "shape needs more scratch than SSD_NOALLOC_SCRATCH_BYTES";
+    case SSD_ERR_BAD_PARENT: return "a beam's parent is outside 0 .. beams - 1";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,499 @@
+// ssd_beam.cu -- beam search for a recurrent model: the selection of the best continuations
+// over beams and vocabulary, and the reordering of the beams' states that follows it.
+//
+// Selection.  With lse_i = log sum_w exp(x[i,w]) of beam i's logits, the continuations' scores
+// are scores[i] + (x[i,w] - lse_i); the best `count` over all (i, w) are wanted, ties to the
+// lowest i * vocab + w.  The logits are read once:
+//   1. blocks of 256 threads, several to a row of logits.  A thread goes over its elements
+//      once and keeps their running maximum, its place, and the running sum of exp(x - R) with
+//      R a multiple of 128 near the maximum.  Each term is a function of x alone (R is the same
+//      for all of a usual row) and the sum is held in 64 bits, so equal rows have equal sums
+//      however they are cut among threads, and equal scores tie.  Let K be the count-th best of the threads' maxima: an element among
+//      the row's best is at or above K and belongs to one of the `count` threads whose maximum
+//      is (count other threads would otherwise each hold a better one), so those threads alone
+//      go over their elements (some dozens, still in cache) a second time and hand on what is
+//      at or above K.
+//   2. one block per batch item joins the sums, forms the scores in 64 bits and picks the best
+//      of the rows' sorted lists by the same argument.
+// Bound by HBM on the logits for large batches, by the two launches' latency for one row.
+//
+// Reordering.  state[b, i] <- state[b, parents[b, i]] in place: the beams of one batch item
+// exchange rows only among themselves, so a thread that holds the same 16 bytes of all its
+// beams loads what moves, then stores it; nothing needs a second buffer.  Rows that stay are
+// neither read nor written.  Bound by HBM.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <memory>
+#include <new>
+#include <utility>
+
+#include "ssd.h"
+#include "ssd_common.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxBeams = 64;
+constexpr int kMaxSplits = 64;
+constexpr int kPerThread = 128;  // elements of a row a thread takes at most
+
+// Whole numbers in the order of the values (-0 and 0 equal; 0 is below every value but NaNs).
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// A candidate's rank as one whole number: a larger value first, then a lower place.  0 is "none".
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t at) {
+  return (uint64_t)ordered(v) << 32 | (uint32_t)~at;
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t o = (uint32_t)(k >> 32);
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ uint32_t key_place(uint64_t k) { return ~(uint32_t)k; }
+
+struct Select {
+  int beams, vocab, count, splits, per_split;  // per_split: elements of a row in one block
+  const void* logits;
+  const float* scores;
+  const uint8_t* finished;
+  int eos;
+  // of each row and split: R, the sum of exp(x - R), the best `count` keys
+  float* row_ref;
+  double* row_sum;
+  uint64_t* keys;
+  float* out_scores;
+  int32_t *out_tokens, *out_parents;
+};
+
+template <typename T>
+struct Vec {
+  static constexpr int n = 16 / sizeof(T);
+  T v[n];
+};
+
+// Elements [8 j, 8 j + 8) (fp32: 4) of the flat logits, those outside [lo, hi) as -inf.
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* logits, int64_t j, int64_t lo, int64_t hi,
+                                         float (&x)[Vec<T>::n]) {
+  constexpr int n = Vec<T>::n;
+  const int64_t e0 = j * n;
+  if (e0 >= lo && e0 + n <= hi) {
+    Vec<T> v;
+    *reinterpret_cast<uint4*>(&v) = __ldg(reinterpret_cast<const uint4*>(logits) + j);
+#pragma unroll
+    for (int i = 0; i < n; ++i) x[i] = to_f(v.v[i]);
+  } else {  // the range begins or ends inside this vector
+#pragma unroll
+    for (int i = 0; i < n; ++i) x[i] = e0 + i >= lo && e0 + i < hi ? to_f(logits[e0 + i]) : -INFINITY;
+  }
+}
+
+// exp(d) for d <= 64, 0 from -200 down, NaN for NaN and +infinity.  The product d * log2(e) is
+// taken with the rounding error it leaves, so the relative error is that of 2^x alone.
+__device__ __forceinline__ float exp_term(float d) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(-200.f));
+  constexpr float kL = 1.44269502162933349609375f, kLow = 1.92596299112661746887e-8f;
+  const float y = d * kL;
+  const float low = fmaf(d, kLow, fmaf(d, kL, -y));
+  float t;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(y));
+  return fmaf(t, low * 0.693147180559945f, t);
+}
+
+// Rank of `mine` among keys[0 .. n): how many are larger.
+__device__ __forceinline__ int rank_of(uint64_t mine, const uint64_t* keys, int n) {
+  int r = 0;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) r += keys[i] > mine;
+  return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
+  constexpr int n = Vec<T>::n;
+  extern __shared__ uint64_t s_list[];  // count * elements per thread
+  __shared__ uint64_t s_key[kThreads];
+  __shared__ double s_sum[kThreads / 32];
+  __shared__ float s_max[kThreads / 32];
+  __shared__ uint64_t s_limit;
+  __shared__ int s_n;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x / a.splits;
+  const int split = blockIdx.x % a.splits;
+  const T* logits = static_cast<const T*>(a.logits);
+  const int64_t start = row * a.vocab;  // of the row in the flat array
+  const int64_t lo = start + (int64_t)split * a.per_split;
+  const int64_t hi = min(start + a.vocab, lo + a.per_split);
+  const int64_t j0 = lo / n, j1 = (hi + n - 1) / n;  // 16-byte vectors that hold the range
+
+  float m = -INFINITY, R = -INFINITY;
+  double s = 0.0;
+  int64_t best = -1;
+  for (int64_t j = j0 + tid; j < j1; j += kThreads) {
+    float x[n];
+    load_vec(logits, j, lo, hi, x);
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < n; ++i) top = fmaxf(top, x[i]);
+    if (top > m) {
+#pragma unroll
+      for (int i = n - 1; i >= 0; --i)
+        if (x[i] == top) best = j * n + i;
+      m = top;
+      if (top - R > 64.f) {  // the first value, or a far larger one
+        const float to = 128.f * rintf(top * (1.f / 128.f));
+        s *= exp((double)R - (double)to);
+        R = to;
+      }
+    }
+    const float ref = R == -INFINITY ? 0.f : R;
+#pragma unroll
+    for (int i = 0; i < n; ++i) s += (double)exp_term(x[i] - ref);  // NaN from an infinite or NaN logit on
+  }
+  // a thread without an element above -inf has no key
+  const uint64_t mine = best >= 0 ? key_of(m, (uint32_t)(best - start)) : 0;
+  float bm = R;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+  if (lane == 0) s_max[warp] = bm;
+  s_key[tid] = mine;
+  if (tid == 0) s_n = 0, s_limit = 1;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) bm = fmaxf(bm, s_max[w]);
+  double sum = s == 0.0 ? 0.0 : s * exp((double)R - (double)bm);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[warp] = sum;
+  const int r = mine ? rank_of(mine, s_key, kThreads) : kThreads;
+  if (r == a.count - 1) s_limit = mine;
+  __syncthreads();
+  if (r < a.count) {
+    const uint64_t limit = s_limit;
+    for (int64_t j = j0 + tid; j < j1; j += kThreads) {
+      float x[n];
+      load_vec(logits, j, lo, hi, x);
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        if (!(x[i] > -INFINITY)) continue;
+        const uint64_t k = key_of(x[i], (uint32_t)(j * n + i - start));
+        if (k >= limit) s_list[atomicAdd(&s_n, 1)] = k;
+      }
+    }
+  }
+  __syncthreads();
+  const int got = s_n;
+  uint64_t* out = a.keys + (int64_t)blockIdx.x * a.count;
+  for (int e = tid; e < got; e += kThreads) {
+    const uint64_t k = s_list[e];
+    const int at = rank_of(k, s_list, got);
+    if (at < a.count) out[at] = k;
+  }
+  for (int e = got + tid; e < a.count; e += kThreads) out[e] = 0;
+  if (tid == 0) {
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) t += s_sum[w];
+    a.row_ref[blockIdx.x] = bm;
+    a.row_sum[blockIdx.x] = t;
+  }
+}
+
+struct Cand {
+  uint32_t score, beam;  // ordered(score), 0: none
+  uint64_t key;          // of the logit and the token
+};
+__device__ __forceinline__ bool before(const Cand& x, const Cand& y) {
+  if (x.score != y.score) return x.score > y.score;
+  if (x.beam != y.beam) return x.beam < y.beam;
+  return x.key > y.key;
+}
+constexpr Cand kNone{0, 0xFFFFFFFFu, 0};
+
+// Entry e of a list of beam `beam` with the sum `lse`; none where the score is -inf or NaN.
+__device__ __forceinline__ Cand candidate(const Select& a, const uint64_t* keys, int beam, bool first_split, int e,
+                                          double lse, double score, bool finished) {
+  if (finished) {
+    if (first_split && e == 0 && score > -INFINITY)
+      return Cand{ordered((float)score), (uint32_t)beam, key_of(0.f, (uint32_t)a.eos)};
+    return kNone;
+  }
+  const uint64_t k = keys[e];
+  if (!k) return kNone;
+  const float v = (float)(score + ((double)key_value(k) - lse));
+  if (!(v > -INFINITY)) return kNone;
+  return Cand{ordered(v), (uint32_t)beam, k};
+}
+
+// One block per batch item.  Lists: (beam, split), each sorted.  A list's entry among the best
+// `count` is at or above the count-th best of the lists' first entries.
+__global__ void __launch_bounds__(kThreads) beam_merge_kernel(Select a) {
+  extern __shared__ unsigned char s_raw[];
+  const int lists = a.beams * a.splits;
+  double* s_lse = reinterpret_cast<double*>(s_raw);                // beams
+  Cand* s_head = reinterpret_cast<Cand*>(s_lse + kMaxBeams);       // lists
+  Cand* s_cand = s_head + lists;                                   // count * count
+  __shared__ Cand s_limit;
+  __shared__ int s_n;
+  const int tid = threadIdx.x;
+  const int64_t b = blockIdx.x;
+  const int64_t list0 = b * lists;
+  if (tid == 0) s_n = 0, s_limit = Cand{1, 0xFFFFFFFFu, 0};
+  for (int i = tid; i < a.beams; i += kThreads) {
+    float m = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.row_ref[list0 + i * a.splits + s]);
+    double sum = 0.0;
+    for (int s = 0; s < a.splits; ++s) {
+      const int64_t l = list0 + i * a.splits + s;
+      const double part = a.row_sum[l];
+      if (part != 0.0) sum += part * exp((double)a.row_ref[l] - (double)m);
+    }
+    s_lse[i] = (double)m + log(sum);  // a row of -inf alone: -inf + -inf, and no key to use it
+  }
+  for (int i = tid; i < a.count; i += kThreads) {  // what stays where there are too few continuations
+    a.out_scores[b * a.count + i] = -INFINITY;
+    a.out_tokens[b * a.count + i] = max(a.eos, 0);
+    a.out_parents[b * a.count + i] = i % a.beams;
+  }
+  __syncthreads();
+  for (int l = tid; l < lists; l += kThreads) {
+    const int beam = l / a.splits;
+    const bool fin = a.finished && a.finished[b * a.beams + beam];
+    s_head[l] = candidate(a, a.keys + (list0 + l) * a.count, beam, l % a.splits == 0, 0, s_lse[beam],
+                          (double)a.scores[b * a.beams + beam], fin);
+  }
+  __syncthreads();
+  for (int l0 = 0; l0 < lists; l0 += kThreads) {
+    const int l = l0 + tid;
+    if (l < lists && s_head[l].score) {
+      int r = 0;
+      for (int i = 0; i < lists; ++i) r += before(s_head[i], s_head[l]);
+      if (r == a.count - 1) s_limit = s_head[l];
+    }
+  }
+  __syncthreads();
+  const Cand limit = s_limit;
+  for (int l = tid; l < lists; l += kThreads) {
+    if (!s_head[l].score || before(limit, s_head[l])) continue;  // below the limit from the start
+    const int beam = l / a.splits;
+    const bool fin = a.finished && a.finished[b * a.beams + beam];
+    for (int e = 0; e < a.count; ++e) {
+      const Cand c = candidate(a, a.keys + (list0 + l) * a.count, beam, l % a.splits == 0, e, s_lse[beam],
+                               (double)a.scores[b * a.beams + beam], fin);
+      if (!c.score || before(limit, c)) break;
+      s_cand[atomicAdd(&s_n, 1)] = c;
+    }
+  }
+  __syncthreads();
+  const int got = s_n;
+  for (int e = tid; e < got; e += kThreads) {
+    const Cand c = s_cand[e];
+    int r = 0;
+    for (int i = 0; i < got; ++i) r += before(s_cand[i], c);
+    if (r < a.count) {
+      a.out_scores[b * a.count + r] = key_value((uint64_t)c.score << 32);
+      a.out_tokens[b * a.count + r] = (int32_t)key_place(c.key);
+      a.out_parents[b * a.count + r] = (int32_t)c.beam;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- reordering
+constexpr int kMaxBuffers = 128;
+constexpr int kReorderThreads = 256;
+
+struct Reorder {
+  const int32_t* parents;
+  unsigned int* status;
+  int beams, nbuf;
+  int64_t batch;
+  struct {
+    void* base;
+    int64_t row;       // units in a row
+    int64_t first;     // first block of this buffer
+    int tiles;         // blocks per batch item
+  } buf[kMaxBuffers];
+};
+
+// Block: one batch item and kReorderThreads units' columns of one buffer.
+template <typename V, int MAXB>
+__global__ void __launch_bounds__(kReorderThreads) state_reorder_kernel(const __grid_constant__ Reorder a) {
+  __shared__ int s_src[MAXB];
+  int i = 0;
+  {
+    int lo = 0, hi = a.nbuf - 1;  // the last buffer that begins at or before this block
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.buf[mid].first <= (int64_t)blockIdx.x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    i = lo;
+  }
+  const int64_t local = (int64_t)blockIdx.x - a.buf[i].first;
+  const int tiles = a.buf[i].tiles;
+  const int64_t b = local / tiles, row = a.buf[i].row;
+  const int64_t col = (local % tiles) * kReorderThreads + threadIdx.x;
+  if (threadIdx.x < MAXB) {
+    int p = threadIdx.x;
+    if (p < a.beams) {
+      p = a.parents[b * a.beams + p];
+      if (p < 0 || p >= a.beams) {  // leave the row as it is and say so
+        p = threadIdx.x;
+        atomicOr(a.status, kStatusBadParent);
+      }
+    }
+    s_src[threadIdx.x] = p;
+  }
+  __syncthreads();
+  if (col >= row) return;
+  V* base = static_cast<V*>(a.buf[i].base) + b * a.beams * row + col;
+  V v[MAXB];
+#pragma unroll
+  for (int k = 0; k < MAXB; ++k)
+    if (k < a.beams && s_src[k] != k) v[k] = base[s_src[k] * row];
+#pragma unroll
+  for (int k = 0; k < MAXB; ++k)
+    if (k < a.beams && s_src[k] != k) base[k * row] = v[k];
+}
+
+template <typename V>
+cudaError_t launch_reorder(Reorder& a, cudaStream_t st) {
+  int64_t blocks = 0;
+  for (int i = 0; i < a.nbuf; ++i) {
+    a.buf[i].row /= (int64_t)sizeof(V);
+    a.buf[i].first = blocks;
+    a.buf[i].tiles = (int)((a.buf[i].row + kReorderThreads - 1) / kReorderThreads);
+    blocks += a.batch * a.buf[i].tiles;
+  }
+  if (blocks > ((int64_t)1 << 31) - 1) return cudaErrorInvalidConfiguration;
+  if (blocks == 0) return cudaSuccess;
+  if (a.beams <= 4)
+    state_reorder_kernel<V, 4><<<(unsigned)blocks, kReorderThreads, 0, st>>>(a);
+  else if (a.beams <= 8)
+    state_reorder_kernel<V, 8><<<(unsigned)blocks, kReorderThreads, 0, st>>>(a);
+  else if (sizeof(V) == 16 || a.beams <= 16)
+    state_reorder_kernel<V, 16><<<(unsigned)blocks, kReorderThreads, 0, st>>>(a);
+  else if constexpr (sizeof(V) < 16)
+    state_reorder_kernel<V, kMaxBeams><<<(unsigned)blocks, kReorderThreads, 0, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" int ssd_beam_select(int64_t batch, int64_t beams, int64_t vocab, ssd_dtype logits_dtype, const void* logits,
+                               const float* scores, const uint8_t* finished, int32_t eos, int64_t count,
+                               float* out_scores, int32_t* out_tokens, int32_t* out_parents, ssd_stream_t stream) {
+  using namespace ssd;
+  if (batch < 0 || beams <= 0 || vocab <= 0 || count <= 0) return SSD_ERR_INVALID_ARG;
+  if (logits_dtype != SSD_F32 && logits_dtype != SSD_BF16) return SSD_ERR_INVALID_ARG;
+  if (beams > kMaxBeams || count > kMaxBeams || vocab > (1 << 20) || batch > (1 << 24)) return SSD_ERR_UNSUPPORTED;
+  if (finished && (eos < 0 || eos >= vocab)) return SSD_ERR_INVALID_ARG;
+  if (batch == 0) return SSD_OK;
+  if (!logits || !scores || !out_scores || !out_tokens || !out_parents) return SSD_ERR_INVALID_ARG;
+  for (const void* p : {logits, (const void*)scores, (const void*)finished, (const void*)out_scores,
+                        (const void*)out_tokens, (const void*)out_parents})
+    if (p && ((uintptr_t)p & 15u)) return SSD_ERR_MISALIGNED;
+  const int64_t rows = batch * beams;
+  // Splits of a row: enough blocks to fill the GPU, 2048 elements or more in each, and at
+  // most kPerThread elements a thread.
+  const int64_t fill = (8 * (int64_t)device_sm_count() + rows - 1) / rows;
+  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(fill, vocab / 2048));
+  splits = std::min<int64_t>(splits, kMaxSplits);
+  splits = std::max<int64_t>(splits, (vocab + kThreads * kPerThread - 1) / (kThreads * kPerThread));
+  const int64_t per_split = ((vocab + splits - 1) / splits + 7) & ~(int64_t)7;
+  splits = (vocab + per_split - 1) / per_split;
+  if (rows * splits > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
+  Select a{};
+  a.beams = (int)beams, a.vocab = (int)vocab, a.count = (int)count, a.splits = (int)splits, a.per_split = (int)per_split;
+  a.logits = logits, a.scores = scores, a.finished = finished, a.eos = finished ? eos : std::max(eos, -1);
+  a.out_scores = out_scores, a.out_tokens = out_tokens, a.out_parents = out_parents;
+  const int es = logits_dtype == SSD_BF16 ? 2 : 4, per_vec = 16 / es;
+  // vectors of a block's range (its ends may share one with a neighbour), per thread
+  const int64_t vecs = per_split / per_vec + 2;
+  const size_t list_bytes = sizeof(uint64_t) * (size_t)count * per_vec * (size_t)((vecs + kThreads - 1) / kThreads);
+  const size_t merge_bytes = sizeof(double) * kMaxBeams + sizeof(Cand) * ((size_t)beams * splits + (size_t)count * count);
+  if (list_bytes > 200 * 1024 || merge_bytes > 200 * 1024) return SSD_ERR_UNSUPPORTED;
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  const size_t n = (size_t)(rows * splits);
+  const size_t o_sum = up(n * sizeof(float)), o_keys = o_sum + up(n * sizeof(double)),
+               total = o_keys + up(n * (size_t)count * sizeof(uint64_t));
+  cudaStream_t st = (cudaStream_t)stream;
+  char* ws = nullptr;
+  if (scratch_alloc((void**)&ws, total, st) != cudaSuccess) return SSD_ERR_CUDA;
+  a.row_ref = (float*)ws, a.row_sum = (double*)(ws + o_sum), a.keys = (uint64_t*)(ws + o_keys);
+  auto* rows_fn = logits_dtype == SSD_BF16 ? beam_rows_kernel<__nv_bfloat16> : beam_rows_kernel<float>;
+  cudaError_t e = cudaSuccess;
+  if (list_bytes > 40 * 1024)
+    e = cudaFuncSetAttribute(rows_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)list_bytes);
+  if (e == cudaSuccess && merge_bytes > 40 * 1024)
+    e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_bytes);
+  if (e == cudaSuccess) {
+    rows_fn<<<(unsigned)n, kThreads, list_bytes, st>>>(a);
+    beam_merge_kernel<<<(unsigned)batch, kThreads, merge_bytes, st>>>(a);
+    count_launches(2);
+    e = cudaGetLastError();
+  }
+  const cudaError_t e2 = cudaFreeAsync(ws, st);
+  return e != cudaSuccess || e2 != cudaSuccess ? SSD_ERR_CUDA : SSD_OK;
+}
+
+extern "C" int ssd_state_reorder(int64_t batch, int64_t beams, const int32_t* parents, int64_t nbuf,
+                                 void* const* buffers, const int64_t* row_bytes, ssd_stream_t stream) {
+  using namespace ssd;
+  if (batch < 0 || beams <= 0 || nbuf < 0) return SSD_ERR_INVALID_ARG;
+  if (beams > kMaxBeams || batch > (1 << 24) || nbuf > (1 << 20)) return SSD_ERR_UNSUPPORTED;
+  if (batch == 0 || nbuf == 0) return SSD_OK;
+  if (!parents || !buffers || !row_bytes) return SSD_ERR_INVALID_ARG;
+  if ((uintptr_t)parents & 3u) return SSD_ERR_MISALIGNED;
+  typedef std::pair<uintptr_t, uintptr_t> Span;
+  std::unique_ptr<Span[]> spans(new (std::nothrow) Span[nbuf]);
+  if (!spans) return SSD_ERR_CUDA;
+  int64_t n = 0;
+  for (int64_t i = 0; i < nbuf; ++i) {
+    if (row_bytes[i] < 0) return SSD_ERR_INVALID_ARG;
+    if (row_bytes[i] == 0) continue;
+    if (!buffers[i]) return SSD_ERR_INVALID_ARG;
+    if ((uintptr_t)buffers[i] & 15u) return SSD_ERR_MISALIGNED;
+    if (row_bytes[i] > ((int64_t)1 << 38) / (batch * beams)) return SSD_ERR_UNSUPPORTED;
+    spans[n++] = Span((uintptr_t)buffers[i], (uintptr_t)buffers[i] + (uintptr_t)(batch * beams * row_bytes[i]));
+  }
+  std::sort(spans.get(), spans.get() + n);
+  for (int64_t i = 1; i < n; ++i)
+    if (spans[i].first < spans[i - 1].second) return SSD_ERR_INVALID_ARG;  // one buffer would be moved twice
+  unsigned int* status = device_status_word();
+  if (!status) return SSD_ERR_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  // buffers whose rows are whole 16-byte units, then those of 4-byte units, then the rest; more
+  // than 16 beams go by 4 bytes, so that a thread can hold one unit of each
+  for (int unit : {16, 4, 1}) {
+    Reorder a{};
+    a.parents = parents, a.status = status, a.beams = (int)beams, a.batch = batch;
+    for (int64_t i = 0; i <= nbuf; ++i) {
+      if (a.nbuf && (i == nbuf || a.nbuf == kMaxBuffers)) {
+        const cudaError_t e = unit == 16 ? launch_reorder<uint4>(a, st)
+                              : unit == 4 ? launch_reorder<uint32_t>(a, st)
+                                          : launch_reorder<uint8_t>(a, st);
+        if (e == cudaErrorInvalidConfiguration) return SSD_ERR_UNSUPPORTED;
+        if (e != cudaSuccess) return SSD_ERR_CUDA;
+        a.nbuf = 0;
+      }
+      if (i == nbuf || row_bytes[i] == 0) continue;
+      const int own = row_bytes[i] % 16 == 0 && beams <= 16 ? 16 : row_bytes[i] % 4 == 0 ? 4 : 1;
+      if (own != unit) continue;
+      a.buf[a.nbuf].base = buffers[i];
+      a.buf[a.nbuf].row = row_bytes[i];
+      ++a.nbuf;
+    }
+  }
+  return SSD_OK;
+}

@@ -10,7 +10,7 @@
 namespace ssd {
 
 // Status bits OR-ed into the per-device status word by kernels.
-enum : unsigned int { kStatusBadSeqlens = 1u, kStatusTimeout = 2u };
+enum : unsigned int { kStatusBadSeqlens = 1u, kStatusTimeout = 2u, kStatusBadParent = 4u };
 
 // One chunk of one sequence: tokens [t0, t0 + len) of sequence `seq`, the
 // `idx`-th chunk of that sequence.  Chunks never straddle a sequence boundary:
@@ -106,6 +106,11 @@ void count_launches(int n);
 
 // Address of the current device's status word (looked up once per device), or null.
 unsigned int* device_status_word();
+
+// Stream-ordered scratch from the library's pool on the current device (free it with
+// cudaFreeAsync on the same stream), and the device's number of SMs.
+cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t st);
+int device_sm_count();
 
 // ssd_forward's shape and chunk rules (and the optional host cu_seqlens check), no launch.
 int check_shape(const ssd_shape* s, bool packed, int chunk);

@@ -1,0 +1,525 @@
+// ssd_linattn_api.cu -- linear attention with a decay for each head: the entry points, the
+// choice of windows, the gradients' plan and the kernels that finish them, and the
+// single-token step.
+//
+// Gradients.  With D_t the gradient of the state S_t (D_t = a_{t+1} D_{t+1} + scale dy_t q_t^T,
+// from dfinal after the last token),
+//   dq_t = scale S_t^T dy_t,   dk_t = D_t^T v_t,   dv_t = D_t k_t,   dinit = a_1 D_1,
+// and each of the first three is the operator again with its operands exchanged: dq is the
+// pass (query, key, value) = (dy, v, k) in the order of the tokens from init^T; dk is
+// (v, dy, q) and dv is (k, q, dy) against the order of the tokens from dfinal.  So the
+// backward pass is three passes of the forward kernel and keeps nothing from the forward
+// pass.  The decay's gradient a_t <D_t, S_{t-1}> is the difference of what q_t.dq_t and
+// k_t.dk_t count (pairs i >= j with i at or after t, minus those with j at or after t):
+//   dl_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <D_end, S_end>
+// summed in 64 bits over windows of at most 1024 tokens, with <D, S> taken anew at every
+// window's end, so that rounding errors do not pile up over a long sequence.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "ssd.h"
+#include "ssd_common.cuh"
+#include "ssd_linattn.cuh"
+
+namespace ssd {
+namespace {
+
+// ------------------------------------------------------------------ finishing the gradients
+struct LaGrad {
+  int64_t tokens, seqlen;
+  int nseq, H, size;  // size: NK * PV
+  const int32_t* cu;
+  int window, dense_windows;
+  const LaWindow* win;
+  const int32_t* win_count;
+  const float *s_end, *d_end;     // (window, H, size): S after the window, and its gradient
+  const float *q_dots, *k_dots;   // (slices, tokens, H)
+  int q_slices, k_slices;
+  const float* log_decay;
+  int per_token;
+  float* out;      // (tokens, H), or null:
+  double* parts;   // (window, H) sums over the window's tokens
+};
+
+constexpr int kGradThreads = 128;
+
+__device__ __forceinline__ double block_sum(double v, double* warp_sums) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kGradThreads / 32; ++w) s += warp_sums[w];
+  return s;
+}
+
+// One block per window and head: <D, S> at the window's end, then the sums towards its start.
+__global__ void __launch_bounds__(kGradThreads) la_decay_grad_kernel(LaGrad a) {
+  __shared__ double s_warp[kGradThreads / 32];
+  const int w = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t t0;
+  int len;
+  if (a.cu) {
+    if (w >= *a.win_count) return;  // (and where the offsets were invalid: -1)
+    t0 = a.win[w].t0, len = a.win[w].len;
+  } else {
+    t0 = (int64_t)(w / a.dense_windows) * a.seqlen + (int64_t)(w % a.dense_windows) * a.window;
+    len = (int)min((int64_t)a.window, a.seqlen - (int64_t)(w % a.dense_windows) * a.window);
+  }
+  if (len <= 0) {
+    if (a.parts && tid == 0) a.parts[(int64_t)w * a.H + h] = 0.0;
+    return;
+  }
+  const float* s = a.s_end + ((int64_t)w * a.H + h) * a.size;
+  const float* d = a.d_end + ((int64_t)w * a.H + h) * a.size;
+  double v = 0.0;
+  for (int e = tid; e < a.size; e += kGradThreads) v += (double)s[e] * (double)d[e];
+  double carry = block_sum(v, s_warp);
+  double total = 0.0;
+  for (int hi = len; hi > 0; hi -= kGradThreads) {  // 128 tokens at a time, from the window's end
+    const int i = hi - 1 - tid;                      // thread 0: the last one
+    const int64_t t = t0 + i;
+    double x = 0.0;
+    if (i >= 0) {
+      for (int q = 0; q < a.q_slices; ++q) x += (double)a.q_dots[((int64_t)q * a.tokens + t) * a.H + h];
+      for (int k = 0; k < a.k_slices; ++k) x -= (double)a.k_dots[((int64_t)k * a.tokens + t) * a.H + h];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    double before = 0.0, all = 0.0;
+#pragma unroll
+    for (int k = 0; k < kGradThreads / 32; ++k) {
+      if (k < warp) before += s_warp[k];
+      all += s_warp[k];
+    }
+    if (i >= 0) {
+      const double l = (double)a.log_decay[a.per_token ? t * a.H + h : h] * 1.4426950408889634;
+      const double g = l <= kLaLogMin ? 0.0 : carry + before + x;  // a decay of zero has no gradient in its log
+      if (a.out) a.out[t * a.H + h] = (float)g;
+      total += g;
+    }
+    carry += all;
+  }
+  if (a.parts) {
+    total = block_sum(total, s_warp);
+    if (tid == 0) a.parts[(int64_t)w * a.H + h] = total;
+  }
+}
+
+// Constant decays: the windows' sums, one block per head.
+__global__ void __launch_bounds__(kGradThreads) la_decay_total_kernel(const double* parts, int windows, const int32_t* count,
+                                                                      int H, float* out) {
+  __shared__ double s_warp[kGradThreads / 32];
+  const int h = blockIdx.x;
+  const int n = count ? *count : windows;
+  if (n < 0) return;
+  double v = 0.0;
+  for (int w = threadIdx.x; w < n; w += kGradThreads) v += parts[(int64_t)w * H + h];
+  v = block_sum(v, s_warp);
+  if (threadIdx.x == 0) out[h] = (float)v;
+}
+
+// dst[t][g][n] = sum over the group's heads of src[t][h][n], heads in order.
+template <typename T>
+__global__ void __launch_bounds__(256) la_group_sum_kernel(const float* src, T* dst, int64_t total, int N, int hpg,
+                                                           const int32_t* count) {
+  if (count && *count < 0) return;
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < total; e += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t tg = e / N;
+    const int n = (int)(e - tg * N);
+    const float* p = src + tg * hpg * N + n;
+    float v = 0.f;
+    for (int i = 0; i < hpg; ++i) v += p[(int64_t)i * N];
+    dst[e] = from_f<T>(v);
+  }
+}
+
+// ------------------------------------------------------------------------ the step
+struct LaStep {
+  int H, P, N, G, hpg;
+  const void *q, *k, *v;
+  const float* log_decay;
+  int per_row;
+  float scale;
+  float* state;
+  void* y;
+};
+
+constexpr int kStepRows = 8, kStepWarps = 4;
+
+// Grid (rows * H, ceil(P / 32)); 4 warps, each advancing 8 rows of the state, all their loads
+// in flight before the first use.  Lane l owns the columns 4 l .. 4 l + 3 (N <= 128).  The
+// state is read and written once and is nearly all of the bytes: bound by HBM.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kStepWarps * 32) la_step_kernel(LaStep a) {
+  const int64_t bh = blockIdx.x;
+  const int64_t b = bh / a.H;
+  const int h = (int)(bh % a.H), g = h / a.hpg;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int p0 = (blockIdx.y * kStepWarps + warp) * kStepRows, n0 = 4 * lane;
+  float* S = a.state + bh * (int64_t)a.P * a.N;
+  float s[kStepRows][4], vp[kStepRows], q[4], k[4];
+#pragma unroll
+  for (int r = 0; r < kStepRows; ++r) {
+    const int p = p0 + r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[r][j] = 0.f;
+    if (p < a.P) {
+      const float* row = S + (int64_t)p * a.N + n0;
+      if (VEC) {
+        if (n0 < a.N) {
+          const float4 x = *reinterpret_cast<const float4*>(row);
+          s[r][0] = x.x, s[r][1] = x.y, s[r][2] = x.z, s[r][3] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n0 + j < a.N) s[r][j] = row[j];
+      }
+    }
+    vp[r] = p < a.P ? to_f(static_cast<const T*>(a.v)[bh * a.P + p]) : 0.f;
+  }
+  const T* qv = static_cast<const T*>(a.q) + (b * a.G + g) * a.N;
+  const T* kv = static_cast<const T*>(a.k) + (b * a.G + g) * a.N;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    q[j] = n0 + j < a.N ? to_f(qv[n0 + j]) : 0.f;
+    k[j] = n0 + j < a.N ? to_f(kv[n0 + j]) : 0.f;
+  }
+  const float decay = expf(a.log_decay[a.per_row ? bh : h]);
+#pragma unroll
+  for (int r = 0; r < kStepRows; ++r) {
+    const int p = p0 + r;
+    float acc = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s[r][j] = fmaf(decay, s[r][j], vp[r] * k[j]);
+      acc = fmaf(q[j], s[r][j], acc);
+    }
+    if (p < a.P) {
+      float* row = S + (int64_t)p * a.N + n0;
+      if (VEC) {
+        if (n0 < a.N) *reinterpret_cast<float4*>(row) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n0 + j < a.N) row[j] = s[r][j];
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (lane == 0 && p < a.P) static_cast<T*>(a.y)[bh * a.P + p] = from_f<T>(acc * a.scale);
+  }
+}
+
+// ------------------------------------------------------------------------ host side
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+int la_validate(const ssd_shape* s, const int32_t* cu) {
+  if (!s) return SSD_ERR_INVALID_ARG;
+  if (s->batch < 0 || s->seqlen < 0 || s->nheads <= 0 || s->headdim <= 0 || s->dstate <= 0 || s->ngroups <= 0)
+    return SSD_ERR_INVALID_ARG;
+  if (s->io_dtype != SSD_F32 && s->io_dtype != SSD_BF16) return SSD_ERR_INVALID_ARG;
+  if (cu && (s->batch != 1 || s->nseq < 1)) return SSD_ERR_INVALID_ARG;
+  if (s->nheads % s->ngroups) return SSD_ERR_UNSUPPORTED;
+  if (s->headdim > kLaMaxDim || s->dstate > kLaMaxDim || s->nheads > 65535) return SSD_ERR_UNSUPPORTED;
+  if (s->batch > (1 << 30) || s->seqlen > (1 << 30) || (cu && s->nseq > (1 << 24))) return SSD_ERR_UNSUPPORTED;
+  const int64_t tokens = s->batch * s->seqlen, rows = cu ? s->nseq : s->batch;
+  if (tokens > ((int64_t)1 << 30) || rows > (1 << 24)) return SSD_ERR_UNSUPPORTED;
+  // the largest grid: windows of 128 tokens, two slices a head
+  if ((tokens / 128 + rows + 1) * s->nheads * 2 > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
+  if (s->cu_seqlens_host && cu) {
+    const int32_t* c = s->cu_seqlens_host;
+    if (c[0] != 0 || (int64_t)c[s->nseq] != tokens) return SSD_ERR_BAD_SEQLENS;
+    for (int64_t i = 1; i <= s->nseq; ++i)
+      if (c[i] < c[i - 1]) return SSD_ERR_BAD_SEQLENS;
+  }
+  return SSD_OK;
+}
+
+bool la_aligned(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (p && ((uintptr_t)p & 15u)) return false;
+  return true;
+}
+
+struct Plan {
+  int window, dense_windows, max_windows;
+  bool segmented, table;
+};
+
+// Windows.  A sequence runs on one CTA per head and 64 value rows; where that leaves SMs idle
+// (few sequences and heads, long sequences) it is cut into windows that run side by side,
+// from states that a pass over key and value alone and a scan over the windows give.
+Plan make_plan(const ssd_shape* s, const int32_t* cu, int slices, bool dump) {
+  const int64_t tokens = s->batch * s->seqlen, rows = cu ? s->nseq : s->batch;
+  const int64_t resident = 3 * (int64_t)device_sm_count();
+  const int64_t lanes = s->nheads * slices;  // CTAs per sequence or window
+  Plan p{};
+  p.window = 512;
+  p.segmented = false;
+  // a packed batch may hold one long sequence among short ones: only many sequences fill the
+  // GPU whatever their lengths
+  const int64_t enough = cu ? 4 * resident : resident;
+  const int64_t mean = rows ? tokens / rows : 0;
+  if (rows * lanes < enough && (cu ? tokens > 256 : mean > 256)) {
+    p.segmented = true;
+    p.window = 1024;
+    while (p.window > 128 && tokens / p.window * lanes < 2 * resident) p.window /= 2;
+  }
+  p.dense_windows = (int)std::max<int64_t>(1, (s->seqlen + p.window - 1) / p.window);
+  const int64_t most = cu ? tokens / p.window + rows : rows * p.dense_windows;
+  p.max_windows = (int)most;
+  p.table = cu != nullptr;
+  (void)dump;
+  return p;
+}
+
+// One pass: the windows' states first where it is segmented.
+cudaError_t run_pass(LaPass p, bool bf16, bool exact, float* carry, float* window_decay, cudaStream_t st) {
+  p.carry = carry;
+  p.window_decay = window_decay;
+  if (p.segmented) {
+    LaPass own = p;
+    own.states_only = 1;
+    own.dump = nullptr, own.last = nullptr, own.dot = nullptr;
+    cudaError_t e = launch_la_general(own, bf16, exact, st);
+    if (e == cudaSuccess) e = launch_la_scan(p, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_la_general(p, bf16, exact, st);
+}
+
+struct TableLayout {
+  size_t win, first, count, total;
+  TableLayout(const Plan& p, int64_t rows, size_t base) {
+    win = base;
+    first = win + (p.table ? up256(sizeof(LaWindow) * (size_t)p.max_windows) : 0);
+    count = first + (p.table ? up256(sizeof(int32_t) * (size_t)(rows + 1)) : 0);
+    total = count + (p.table ? 256 : 0);
+  }
+};
+
+void set_common(LaPass& p, const ssd_shape* s, const Plan& plan, const int32_t* cu, char* ws, const TableLayout& t,
+                const float* log_decay, int per_token, float scale) {
+  p.tokens = s->batch * s->seqlen;
+  p.seqlen = s->seqlen;
+  p.nseq = (int)(cu ? s->nseq : s->batch);
+  p.H = (int)s->nheads;
+  p.cu = cu;
+  p.window = plan.window;
+  p.dense_windows = plan.dense_windows;
+  p.max_windows = plan.max_windows;
+  if (plan.table) {
+    p.win = (const LaWindow*)(ws + t.win);
+    p.first_win = (const int32_t*)(ws + t.first);
+    p.win_count = (const int32_t*)(ws + t.count);
+  }
+  p.log_decay = log_decay;
+  p.per_token = per_token;
+  p.scale = scale;
+  p.segmented = plan.segmented;
+}
+
+cudaError_t build_table(const ssd_shape* s, const Plan& plan, const int32_t* cu, char* ws, const TableLayout& t,
+                        unsigned int* status, cudaStream_t st) {
+  if (!plan.table) return cudaSuccess;
+  LaTable tab{(LaWindow*)(ws + t.win), (int32_t*)(ws + t.first), (int32_t*)(ws + t.count)};
+  return launch_la_table(s->batch * s->seqlen, (int)s->nseq, cu, plan.window, plan.max_windows, tab, status, st);
+}
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" int ssd_linear_attention_forward(const ssd_shape* s, const void* q, const void* k, const void* v,
+                                            const float* log_decay, int decay_per_token, float scale,
+                                            const float* init_state, const int32_t* cu, void* y, float* final_state,
+                                            ssd_stream_t stream) {
+  using namespace ssd;
+  const int rc = la_validate(s, cu);
+  if (rc) return rc;
+  const int64_t tokens = s->batch * s->seqlen, rows = cu ? s->nseq : s->batch;
+  if (!log_decay && (tokens > 0 || !decay_per_token)) return SSD_ERR_INVALID_ARG;
+  if (tokens > 0 && (!q || !k || !v || !y)) return SSD_ERR_INVALID_ARG;
+  if (!la_aligned({q, k, v, log_decay, init_state, cu, y, final_state})) return SSD_ERR_MISALIGNED;
+  if (rows == 0) return SSD_OK;
+  unsigned int* status = device_status_word();
+  if (!status) return SSD_ERR_CUDA;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int P = (int)s->headdim, N = (int)s->dstate, H = (int)s->nheads, hpg = (int)(s->nheads / s->ngroups);
+  const Plan plan = make_plan(s, cu, la_general_slices(P), false);
+  const TableLayout tl(plan, rows, 0);
+  const size_t o_carry = tl.total;
+  const size_t o_dec = o_carry + (plan.segmented ? up256(sizeof(float) * (size_t)plan.max_windows * H * P * N) : 0);
+  const size_t total = o_dec + (plan.segmented ? up256(sizeof(float) * (size_t)plan.max_windows * H) : 0);
+  char* ws = nullptr;
+  if (total && scratch_alloc((void**)&ws, total, st) != cudaSuccess) return SSD_ERR_CUDA;
+  LaPass p{};
+  set_common(p, s, plan, cu, ws, tl, log_decay, decay_per_token, scale);
+  p.query = q, p.key = k, p.value = v;
+  p.q_heads = p.k_heads = (int)s->ngroups, p.v_heads = H;
+  p.q_div = p.k_div = hpg, p.v_div = 1;
+  p.NK = N, p.PV = P;
+  p.start = init_state, p.last = final_state, p.sr = N, p.sc = 1;
+  p.out = y;
+  const bool bf16 = s->io_dtype == SSD_BF16;
+  cudaError_t e = build_table(s, plan, cu, ws, tl, status, st);
+  if (e == cudaSuccess) e = run_pass(p, bf16, false, (float*)(ws + o_carry), (float*)(ws + o_dec), st);
+  const cudaError_t e2 = ws ? cudaFreeAsync(ws, st) : cudaSuccess;
+  return e != cudaSuccess || e2 != cudaSuccess ? SSD_ERR_CUDA : SSD_OK;
+}
+
+extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy, const void* q, const void* k,
+                                             const void* v, const float* log_decay, int decay_per_token, float scale,
+                                             const float* init_state, const float* dfinal_state, const int32_t* cu,
+                                             void* dq, void* dk, void* dv, float* dlog_decay, float* dinit_state,
+                                             ssd_stream_t stream) {
+  using namespace ssd;
+  const int rc = la_validate(s, cu);
+  if (rc) return rc;
+  const int64_t tokens = s->batch * s->seqlen, rows = cu ? s->nseq : s->batch;
+  if (!log_decay && (tokens > 0 || !decay_per_token)) return SSD_ERR_INVALID_ARG;
+  if (tokens > 0 && (!dy || !q || !k || !v || !dq || !dk || !dv)) return SSD_ERR_INVALID_ARG;
+  if (!la_aligned({dy, q, k, v, log_decay, init_state, dfinal_state, cu, dq, dk, dv, dlog_decay, dinit_state}))
+    return SSD_ERR_MISALIGNED;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int P = (int)s->headdim, N = (int)s->dstate, H = (int)s->nheads, G = (int)s->ngroups, hpg = H / G;
+  if (rows == 0) {
+    if (dlog_decay && !decay_per_token && cudaMemsetAsync(dlog_decay, 0, sizeof(float) * H, st) != cudaSuccess)
+      return SSD_ERR_CUDA;
+    return SSD_OK;
+  }
+  unsigned int* status = device_status_word();
+  if (!status) return SSD_ERR_CUDA;
+  const bool bf16 = s->io_dtype == SSD_BF16, decay_grad = dlog_decay != nullptr, shared = hpg > 1;
+  const int p_slices = la_general_slices(P), n_slices = la_general_slices(N);
+  const Plan plan = make_plan(s, cu, std::min(p_slices, n_slices), decay_grad);
+  const size_t W = (size_t)plan.max_windows, state = (size_t)H * P * N, th = (size_t)tokens * H;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up256(bytes);
+    return here;
+  };
+  const TableLayout tl(plan, rows, 0);
+  at = tl.total;
+  const size_t o_carry = take(plan.segmented ? 4 * W * state : 0);
+  const size_t o_dec = take(plan.segmented ? 4 * W * H : 0);
+  const size_t o_send = take(decay_grad ? 4 * W * state : 0), o_dend = take(decay_grad ? 4 * W * state : 0);
+  const size_t o_qdot = take(decay_grad ? 4 * th * n_slices : 0), o_kdot = take(decay_grad ? 4 * th * n_slices : 0);
+  const size_t o_parts = take(decay_grad && !decay_per_token ? 8 * W * H : 0);
+  const size_t o_part = take(shared ? 4 * th * N : 0);
+  char* ws = nullptr;
+  if (at && scratch_alloc((void**)&ws, at, st) != cudaSuccess) return SSD_ERR_CUDA;
+  float *carry = (float*)(ws + o_carry), *dec = (float*)(ws + o_dec);
+  cudaError_t e = build_table(s, plan, cu, ws, tl, status, st);
+  const int32_t* count = plan.table ? (const int32_t*)(ws + tl.count) : nullptr;
+
+  LaPass base{};
+  set_common(base, s, plan, cu, ws, tl, log_decay, decay_per_token, scale);
+  auto group_sum = [&](void* dst) {
+    const int64_t n = tokens * G * N;
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 148 * 32);
+    if (n == 0) return cudaSuccess;
+    if (bf16)
+      la_group_sum_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>((const float*)(ws + o_part), (__nv_bfloat16*)dst, n, N, hpg, count);
+    else
+      la_group_sum_kernel<float><<<blocks, 256, 0, st>>>((const float*)(ws + o_part), (float*)dst, n, N, hpg, count);
+    count_launches(1);
+    return cudaGetLastError();
+  };
+  if (e == cudaSuccess) {  // dq = pass (dy, v, k) from init^T
+    LaPass p = base;
+    p.query = dy, p.key = v, p.value = k;
+    p.q_heads = p.k_heads = H, p.v_heads = G, p.q_div = p.k_div = 1, p.v_div = hpg;
+    p.NK = P, p.PV = N;
+    p.start = init_state, p.sr = 1, p.sc = N;
+    p.out = shared ? (void*)(ws + o_part) : dq, p.out_f32 = shared;
+    if (decay_grad) p.dump = (float*)(ws + o_send), p.dot = q, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_qdot);
+    e = run_pass(p, bf16, decay_grad, carry, dec, st);
+    if (e == cudaSuccess && shared) e = group_sum(dq);
+  }
+  if (e == cudaSuccess) {  // dk = pass (v, dy, q), backwards from dfinal^T
+    LaPass p = base;
+    p.reverse = 1;
+    p.query = v, p.key = dy, p.value = q;
+    p.q_heads = p.k_heads = H, p.v_heads = G, p.q_div = p.k_div = 1, p.v_div = hpg;
+    p.NK = P, p.PV = N;
+    p.start = dfinal_state, p.sr = 1, p.sc = N;
+    p.out = shared ? (void*)(ws + o_part) : dk, p.out_f32 = shared;
+    if (decay_grad) p.dump = (float*)(ws + o_dend), p.dot = k, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_kdot);
+    e = run_pass(p, bf16, decay_grad, carry, dec, st);
+    if (e == cudaSuccess && shared) e = group_sum(dk);
+  }
+  if (e == cudaSuccess) {  // dv = pass (k, q, dy), backwards from dfinal; its last state is dinit
+    LaPass p = base;
+    p.reverse = 1;
+    p.query = k, p.key = q, p.value = dy;
+    p.q_heads = p.k_heads = G, p.v_heads = H, p.q_div = p.k_div = hpg, p.v_div = 1;
+    p.NK = N, p.PV = P;
+    p.start = dfinal_state, p.last = dinit_state, p.sr = N, p.sc = 1;
+    p.out = dv;
+    e = run_pass(p, bf16, false, carry, dec, st);
+  }
+  if (e == cudaSuccess && decay_grad) {
+    LaGrad g{};
+    g.tokens = tokens, g.seqlen = s->seqlen, g.nseq = (int)rows, g.H = H, g.size = P * N;
+    g.cu = cu, g.window = plan.window, g.dense_windows = plan.dense_windows;
+    g.win = base.win, g.win_count = base.win_count;
+    g.s_end = (const float*)(ws + o_send), g.d_end = (const float*)(ws + o_dend);
+    g.q_dots = (const float*)(ws + o_qdot), g.k_dots = (const float*)(ws + o_kdot);
+    g.q_slices = g.k_slices = n_slices;
+    g.log_decay = log_decay, g.per_token = decay_per_token;
+    g.out = decay_per_token ? dlog_decay : nullptr;
+    g.parts = decay_per_token ? nullptr : (double*)(ws + o_parts);
+    la_decay_grad_kernel<<<dim3((unsigned)plan.max_windows, (unsigned)H), kGradThreads, 0, st>>>(g);
+    count_launches(1);
+    if (!decay_per_token) {
+      la_decay_total_kernel<<<H, kGradThreads, 0, st>>>(g.parts, plan.max_windows, count, H, dlog_decay);
+      count_launches(1);
+    }
+    e = cudaGetLastError();
+  }
+  const cudaError_t e2 = ws ? cudaFreeAsync(ws, st) : cudaSuccess;
+  return e != cudaSuccess || e2 != cudaSuccess ? SSD_ERR_CUDA : SSD_OK;
+}
+
+extern "C" int ssd_linear_attention_step(const ssd_shape* s, const void* q, const void* k, const void* v,
+                                         const float* log_decay, int decay_per_row, float scale, float* state, void* y,
+                                         ssd_stream_t stream) {
+  using namespace ssd;
+  const int rc = la_validate(s, nullptr);
+  if (rc) return rc;
+  if (s->seqlen != 1) return SSD_ERR_INVALID_ARG;
+  if (s->batch == 0) return SSD_OK;
+  if (!q || !k || !v || !log_decay || !state || !y) return SSD_ERR_INVALID_ARG;
+  if (!la_aligned({q, k, v, log_decay, state, y})) return SSD_ERR_MISALIGNED;
+  LaStep a{};
+  a.H = (int)s->nheads, a.P = (int)s->headdim, a.N = (int)s->dstate, a.G = (int)s->ngroups, a.hpg = a.H / a.G;
+  a.q = q, a.k = k, a.v = v, a.log_decay = log_decay, a.per_row = decay_per_row, a.scale = scale;
+  a.state = state, a.y = y;
+  const int rows = kStepRows * kStepWarps;
+  const dim3 grid((unsigned)(s->batch * s->nheads), (unsigned)((a.P + rows - 1) / rows));
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool vec = a.N % 4 == 0;
+  if (s->io_dtype == SSD_BF16)
+    vec ? la_step_kernel<__nv_bfloat16, true><<<grid, kStepWarps * 32, 0, st>>>(a)
+        : la_step_kernel<__nv_bfloat16, false><<<grid, kStepWarps * 32, 0, st>>>(a);
+  else
+    vec ? la_step_kernel<float, true><<<grid, kStepWarps * 32, 0, st>>>(a)
+        : la_step_kernel<float, false><<<grid, kStepWarps * 32, 0, st>>>(a);
+  count_launches(1);
+  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
