@@ -356,7 +356,8 @@ int ssd_query_status(ssd_stream_t stream);
 const char* ssd_status_string(int status);
 
 /*
- * Kernel path selection, process-wide (not thread-safe; meant for tests and benches):
+ * Kernel path selection of ssd_forward and of linear attention's prompt pass and gradients,
+ * process-wide (not thread-safe; meant for tests and benches):
  *   SSD_PATH_AUTO  the tensor-core (tcgen05) path where the shape supports it, else SIMT
  *   SSD_PATH_SIMT  the general CUDA-core path for every shape and dtype
  *   SSD_PATH_TC    the tensor-core path; shapes it cannot take return SSD_ERR_UNSUPPORTED
@@ -395,7 +396,9 @@ uint64_t ssd_kernel_launch_count(void);
  *              state itself is still written), so the CTAs that wait for it run out of time;
  *   bit 1 (2): CTA 0 keeps back its flag of the barrier after the work split's tile weights
  *              (launches that weigh their tiles in the kernel), so every CTA's wait there
- *              runs out of time and no CTA takes any work.
+ *              runs out of time and no CTA takes any work;
+ *   bit 2 (4): linear attention's tensor-core kernel keeps back the signal that a block's first
+ *              product is done, so its other roles run out of time.
  * Returns SSD_OK, or SSD_ERR_INVALID_ARG for a negative limit or other bits.
  */
 int ssd_set_test_hooks(int64_t wait_limit_cycles, int withhold);

@@ -366,6 +366,9 @@ void count_launches(int n) { g_launches.fetch_add((uint64_t)n); }
 unsigned int* device_status_word() { return status_ptr(); }
 cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t st) { return pool_alloc(ptr, bytes, st); }
 int device_sm_count() { return device_sms(); }
+long long device_wait_limit() { return g_wait_limit.load(); }
+int path_setting() { return g_path.load(); }
+int device_withhold() { return g_withhold_carry.load(); }
 int check_shape(const ssd_shape* s, bool packed, int chunk) {
   const void* f = (const void*)16;  // stands for every required pointer: only shapes are checked
   return validate(s, f, (const float*)f, (const float*)f, f, f, packed ? (const int32_t*)f : nullptr, chunk, f);
@@ -608,7 +611,7 @@ int ssd_profile_dominant(ssd_event_t start, ssd_event_t stop) {
 uint64_t ssd_kernel_launch_count(void) { return g_launches.load(); }
 
 int ssd_set_test_hooks(int64_t wait_limit_cycles, int withhold) {
-  if (wait_limit_cycles < 0 || (withhold & ~3)) return SSD_ERR_INVALID_ARG;
+  if (wait_limit_cycles < 0 || (withhold & ~7)) return SSD_ERR_INVALID_ARG;
   g_wait_limit.store(wait_limit_cycles ? (long long)wait_limit_cycles : kDefaultWaitLimit);
   g_withhold_carry.store(withhold);
   return SSD_OK;

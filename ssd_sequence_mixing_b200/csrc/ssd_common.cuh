@@ -111,6 +111,10 @@ unsigned int* device_status_word();
 // cudaFreeAsync on the same stream), and the device's number of SMs.
 cudaError_t scratch_alloc(void** ptr, size_t bytes, cudaStream_t st);
 int device_sm_count();
+// The bound of a device-side wait in SM cycles, and the test hooks' withheld flags.
+long long device_wait_limit();
+int device_withhold();
+int path_setting();  // SSD_PATH_*
 
 // ssd_forward's shape and chunk rules (and the optional host cu_seqlens check), no launch.
 int check_shape(const ssd_shape* s, bool packed, int chunk);

@@ -75,6 +75,10 @@ cudaError_t launch_la_table(int64_t tokens, int nseq, const int32_t* cu, int win
 // bf16: io type; exact: the products that enter `out` keep fp32 accuracy (needed for dots).
 cudaError_t launch_la_general(const LaPass& p, bool bf16, bool exact, cudaStream_t st);
 int la_general_slices(int PV);
+// The tcgen05 kernel (bf16): whether it takes the pass, and whether its CTAs take two heads each.
+bool la_tc_supports(const LaPass& p);
+bool la_tc_pairs(const LaPass& p);
+cudaError_t launch_la_tc(const LaPass& p, bool exact, cudaStream_t st);
 // carry[w] <- the state before window w (reverse: after it in time), from the windows' own states.
 cudaError_t launch_la_scan(const LaPass& p, cudaStream_t st);
 

@@ -38,7 +38,7 @@ struct LaGrad {
   const int32_t* win_count;
   const float *s_end, *d_end;     // (window, H, size): S after the window, and its gradient
   const float *q_dots, *k_dots;   // (slices, tokens, H)
-  int q_slices, k_slices;
+  int slices;
   const float* log_decay;
   int per_token;
   float* out;      // (tokens, H), or null:
@@ -87,8 +87,10 @@ __global__ void __launch_bounds__(kGradThreads) la_decay_grad_kernel(LaGrad a) {
     const int64_t t = t0 + i;
     double x = 0.0;
     if (i >= 0) {
-      for (int q = 0; q < a.q_slices; ++q) x += (double)a.q_dots[((int64_t)q * a.tokens + t) * a.H + h];
-      for (int k = 0; k < a.k_slices; ++k) x -= (double)a.k_dots[((int64_t)k * a.tokens + t) * a.H + h];
+      for (int n = 0; n < a.slices; ++n) {
+        const int64_t at = ((int64_t)n * a.tokens + t) * a.H + h;
+        x += (double)a.q_dots[at] - (double)a.k_dots[at];
+      }
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -260,46 +262,59 @@ struct Plan {
   bool segmented, table;
 };
 
-// Windows.  A sequence runs on one CTA per head and 64 value rows; where that leaves SMs idle
-// (few sequences and heads, long sequences) it is cut into windows that run side by side,
-// from states that a pass over key and value alone and a scan over the windows give.
-Plan make_plan(const ssd_shape* s, const int32_t* cu, int slices, bool dump) {
+// Windows.  A sequence runs on `lanes` CTAs of which `resident` fit the GPU at once; where that
+// leaves SMs idle (few sequences and heads, long sequences) it is cut into windows that run side
+// by side, from states that a pass over key and value alone and a scan over the windows give.
+// That pass costs about 0.6 of the full one, so the cut pays where
+// 1.6 * units / resident is below the waves of whole units, with a tenth for the scan.
+Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, int64_t resident) {
   const int64_t tokens = s->batch * s->seqlen, rows = cu ? s->nseq : s->batch;
-  const int64_t resident = 3 * (int64_t)device_sm_count();
-  const int64_t lanes = s->nheads * slices;  // CTAs per sequence or window
   Plan p{};
   p.window = 512;
   p.segmented = false;
+  const int64_t mean = rows ? tokens / rows : 0;
+  const double units = (double)rows * (double)lanes;
+  const double waves = (double)((rows * lanes + resident - 1) / resident);
   // a packed batch may hold one long sequence among short ones: only many sequences fill the
   // GPU whatever their lengths
-  const int64_t enough = cu ? 4 * resident : resident;
-  const int64_t mean = rows ? tokens / rows : 0;
-  if (rows * lanes < enough && (cu ? tokens > 256 : mean > 256)) {
+  const bool idle = cu ? units < 4.0 * resident && tokens > 256 : 1.76 * units < waves * resident && mean > 256;
+  if (idle) {
     p.segmented = true;
     p.window = 1024;
-    while (p.window > 128 && tokens / p.window * lanes < 2 * resident) p.window /= 2;
+    while (p.window > 128 && tokens / p.window * lanes < 3 * resident) p.window /= 2;
   }
   p.dense_windows = (int)std::max<int64_t>(1, (s->seqlen + p.window - 1) / p.window);
   const int64_t most = cu ? tokens / p.window + rows : rows * p.dense_windows;
   p.max_windows = (int)most;
   p.table = cu != nullptr;
-  (void)dump;
   return p;
 }
 
+// The tcgen05 kernel takes bf16 operands of whole 16-byte rows; PATH_SIMT keeps to the general one.
+bool wants_tc(const ssd_shape* s) {
+  return s->io_dtype == SSD_BF16 && s->headdim % 8 == 0 && s->dstate % 8 == 0 && path_setting() != SSD_PATH_SIMT;
+}
+Plan plan_for(const ssd_shape* s, const int32_t* cu, bool tc, bool pairs, int slices) {
+  return tc ? make_plan(s, cu, pairs ? s->nheads / 2 : s->nheads, device_sm_count())
+            : make_plan(s, cu, s->nheads * slices, 3 * (int64_t)device_sm_count());
+}
+
 // One pass: the windows' states first where it is segmented.
-cudaError_t run_pass(LaPass p, bool bf16, bool exact, float* carry, float* window_decay, cudaStream_t st) {
+cudaError_t run_pass(LaPass p, bool tc, bool bf16, bool exact, float* carry, float* window_decay, cudaStream_t st) {
   p.carry = carry;
   p.window_decay = window_decay;
+  auto launch = [&](const LaPass& q, bool ex) {
+    return tc && la_tc_supports(q) ? launch_la_tc(q, ex, st) : launch_la_general(q, bf16, ex, st);
+  };
   if (p.segmented) {
     LaPass own = p;
     own.states_only = 1;
     own.dump = nullptr, own.last = nullptr, own.dot = nullptr;
-    cudaError_t e = launch_la_general(own, bf16, exact, st);
+    cudaError_t e = launch(own, false);
     if (e == cudaSuccess) e = launch_la_scan(p, st);
     if (e != cudaSuccess) return e;
   }
-  return launch_la_general(p, bf16, exact, st);
+  return launch(p, exact);
 }
 
 struct TableLayout {
@@ -359,7 +374,9 @@ extern "C" int ssd_linear_attention_forward(const ssd_shape* s, const void* q, c
   if (!status) return SSD_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   const int P = (int)s->headdim, N = (int)s->dstate, H = (int)s->nheads, hpg = (int)(s->nheads / s->ngroups);
-  const Plan plan = make_plan(s, cu, la_general_slices(P), false);
+  const bool tc = wants_tc(s);
+  if (path_setting() == SSD_PATH_TC && !tc) return SSD_ERR_UNSUPPORTED;
+  const Plan plan = plan_for(s, cu, tc, P <= 64 && hpg % 2 == 0, la_general_slices(P));
   const TableLayout tl(plan, rows, 0);
   const size_t o_carry = tl.total;
   const size_t o_dec = o_carry + (plan.segmented ? up256(sizeof(float) * (size_t)plan.max_windows * H * P * N) : 0);
@@ -376,7 +393,7 @@ extern "C" int ssd_linear_attention_forward(const ssd_shape* s, const void* q, c
   p.out = y;
   const bool bf16 = s->io_dtype == SSD_BF16;
   cudaError_t e = build_table(s, plan, cu, ws, tl, status, st);
-  if (e == cudaSuccess) e = run_pass(p, bf16, false, (float*)(ws + o_carry), (float*)(ws + o_dec), st);
+  if (e == cudaSuccess) e = run_pass(p, tc, bf16, false, (float*)(ws + o_carry), (float*)(ws + o_dec), st);
   const cudaError_t e2 = ws ? cudaFreeAsync(ws, st) : cudaSuccess;
   return e != cudaSuccess || e2 != cudaSuccess ? SSD_ERR_CUDA : SSD_OK;
 }
@@ -404,8 +421,11 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
   unsigned int* status = device_status_word();
   if (!status) return SSD_ERR_CUDA;
   const bool bf16 = s->io_dtype == SSD_BF16, decay_grad = dlog_decay != nullptr, shared = hpg > 1;
-  const int p_slices = la_general_slices(P), n_slices = la_general_slices(N);
-  const Plan plan = make_plan(s, cu, std::min(p_slices, n_slices), decay_grad);
+  const bool tc = wants_tc(s);
+  if (path_setting() == SSD_PATH_TC && !tc) return SSD_ERR_UNSUPPORTED;
+  const int slices = std::min(la_general_slices(P), la_general_slices(N));
+  const int dot_slices = tc && tokens > 0 ? (N + 31) / 32 : la_general_slices(N);  // partial dots of a token
+  const Plan plan = plan_for(s, cu, tc, false, slices);
   const size_t W = (size_t)plan.max_windows, state = (size_t)H * P * N, th = (size_t)tokens * H;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -418,7 +438,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
   const size_t o_carry = take(plan.segmented ? 4 * W * state : 0);
   const size_t o_dec = take(plan.segmented ? 4 * W * H : 0);
   const size_t o_send = take(decay_grad ? 4 * W * state : 0), o_dend = take(decay_grad ? 4 * W * state : 0);
-  const size_t o_qdot = take(decay_grad ? 4 * th * n_slices : 0), o_kdot = take(decay_grad ? 4 * th * n_slices : 0);
+  const size_t o_qdot = take(decay_grad ? 4 * th * dot_slices : 0), o_kdot = take(decay_grad ? 4 * th * dot_slices : 0);
   const size_t o_parts = take(decay_grad && !decay_per_token ? 8 * W * H : 0);
   const size_t o_part = take(shared ? 4 * th * N : 0);
   char* ws = nullptr;
@@ -448,7 +468,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
     p.start = init_state, p.sr = 1, p.sc = N;
     p.out = shared ? (void*)(ws + o_part) : dq, p.out_f32 = shared;
     if (decay_grad) p.dump = (float*)(ws + o_send), p.dot = q, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_qdot);
-    e = run_pass(p, bf16, decay_grad, carry, dec, st);
+    e = run_pass(p, tc, bf16, decay_grad, carry, dec, st);
     if (e == cudaSuccess && shared) e = group_sum(dq);
   }
   if (e == cudaSuccess) {  // dk = pass (v, dy, q), backwards from dfinal^T
@@ -460,7 +480,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
     p.start = dfinal_state, p.sr = 1, p.sc = N;
     p.out = shared ? (void*)(ws + o_part) : dk, p.out_f32 = shared;
     if (decay_grad) p.dump = (float*)(ws + o_dend), p.dot = k, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_kdot);
-    e = run_pass(p, bf16, decay_grad, carry, dec, st);
+    e = run_pass(p, tc, bf16, decay_grad, carry, dec, st);
     if (e == cudaSuccess && shared) e = group_sum(dk);
   }
   if (e == cudaSuccess) {  // dv = pass (k, q, dy), backwards from dfinal; its last state is dinit
@@ -471,7 +491,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
     p.NK = N, p.PV = P;
     p.start = dfinal_state, p.last = dinit_state, p.sr = N, p.sc = 1;
     p.out = dv;
-    e = run_pass(p, bf16, false, carry, dec, st);
+    e = run_pass(p, tc, bf16, false, carry, dec, st);
   }
   if (e == cudaSuccess && decay_grad) {
     LaGrad g{};
@@ -480,7 +500,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
     g.win = base.win, g.win_count = base.win_count;
     g.s_end = (const float*)(ws + o_send), g.d_end = (const float*)(ws + o_dend);
     g.q_dots = (const float*)(ws + o_qdot), g.k_dots = (const float*)(ws + o_kdot);
-    g.q_slices = g.k_slices = n_slices;
+    g.slices = dot_slices;
     g.log_decay = log_decay, g.per_token = decay_per_token;
     g.out = decay_per_token ? dlog_decay : nullptr;
     g.parts = decay_per_token ? nullptr : (double*)(ws + o_parts);

@@ -1,0 +1,930 @@
+// ssd_linattn_tc.cu -- the tcgen05 kernel of linear attention with a decay for each head: bf16
+// operands whose dimensions are multiples of 8.
+//
+// The mathematics is that of ssd_linattn.cu: blocks of 64 tokens, everything transposed so that
+// the rows of the value dimension are the 128 rows of a product (lanes of tensor memory):
+//   S1          = query key^T                          64 x 64,   both from shared memory
+//   P           = decay o S1                           to shared memory (bf16)
+//   Yi^T        = S query^T                            128 x 64,  S from tensor memory (bf16)
+//   Ya^T        = value^T P^T                          128 x 64,  both from shared memory
+//   out_i       = row_i Yi_i + Ya_i                    written from tensor memory
+//   dS          = (upd o value)^T key                  128 x NK,  three bf16 planes of
+//                                                      upd o value from tensor memory
+//   S          <- 2^(c_end) S + dS                     S stays in registers, fp32
+// dS does not depend on S, so only the last line is a recurrence; everything else of a block
+// runs while the previous one finishes.
+//
+// One CTA per SM takes one head (up to 128 value rows), or two heads of up to 64 rows each
+// that share query and key, and walks the blocks of its unit.  20 warps, each with one task, so
+// that the tasks of several blocks overlap without any of them being interleaved by hand:
+//   load  (1 warp)   query, key, value tiles by TMA, three stages
+//   mma   (1 warp)   issues every product
+//   gates (2 warps)  a head each: the sums of log-decays in 64 bits and the factors from them
+//   mask  (4 warps)  S1 -> P
+//   decay (4 warps)  value -> the planes of upd o value, by transposing loads
+//   state (8 warps)  dS -> S -> the bf16 planes of S; Yi, Ya -> out
+// Tensor memory (512 columns): S1 64, Yi 64, Ya 64 (two heads 128), dS 128, planes of
+// upd o value 2 x 32, planes of S 64 (`planes` = 3: 2 x 64).
+//
+// With planes = 3 P and S enter their products as three bf16 planes each (fp32 accuracy), which
+// the per-token dot products behind the decay's gradient need.
+//
+// Every wait is bounded; one that runs out stops the CTA's roles, which drain what is in
+// flight, and SSD_ERR_DEVICE_TIMEOUT is recorded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sm100_ptx.cuh"
+#include "ssd.h"
+#include "ssd_common.cuh"
+#include "ssd_linattn.cuh"
+#include "ssd_linattn_dev.cuh"
+#include "ssd_tc.cuh"
+
+namespace ssd {
+namespace {
+
+using namespace sm100;
+
+constexpr int kC = kLaChunk;  // tokens of a block
+constexpr int kAtomBytes = kC * 128;  // 64 tokens x 64 columns of bf16, 128-byte rows
+constexpr int kStages = 3, kGateSlots = 4, kPlanes = 3;
+constexpr int kWarpsTc = 20, kThreadsTc = 32 * kWarpsTc;
+constexpr int kLoadWarp = 0, kMmaWarp = 1, kGateWarp = 2, kMaskWarp = 4, kDecayWarp = 8, kStateWarp = 12;
+
+// tensor memory columns
+constexpr int kColS1 = 0, kColYi = 64, kColYa = 128, kColDs = 256, kColUv = 384, kColSp0 = 448, kColSp1 = 192;
+constexpr int kTmem = 512;
+
+enum Bar {
+  kFull = 0,                     // tiles of a stage have landed
+  kReady = kFull + kStages,      // ... and rows past the sequence's end are zero (decay warps)
+  kFree = kReady + kStages,      // every product that reads the stage is done
+  kS1Full = kFree + kStages, kS1Free,
+  kPFull, kPFree,
+  kUvFull, kUvFree = kUvFull + 2,
+  kDsFull = kUvFree + 2, kDsFree,
+  kSpFull, kSpFree = kSpFull + 2,
+  kYFull = kSpFree + 2, kYFree,
+  kGFull, kGFree = kGFull + kGateSlots,
+  kDrain = kGFree + kGateSlots,
+  kBars
+};
+
+struct Gate {
+  float chi[kC], clo[kC], row[kC], upd[kC];
+  float decay, pad[3];
+};
+
+// A state warp's own staging: 16 tokens x 32 rows of outputs (bf16: 80 bytes a token, fp32: 144;
+// neither pitch has bank conflicts), and 32 tokens x 32 rows of bf16.
+constexpr int kOutBytes = 16 * 144, kOutPitch = 80, kOutPitch32 = 144, kDotBytes = 32 * kOutPitch;
+
+template <int NT, bool PAIR>
+struct TcSmem {
+  static constexpr int kHeads = PAIR ? 2 : 1;
+  static constexpr int kQ = 0, kK = NT / 64 * kAtomBytes, kV = 2 * kK, kStage = kV + 2 * kAtomBytes;
+  static constexpr int kP = kStages * kStage;                       // P: planes, or one per head
+  static constexpr int kGate = kP + (PAIR ? 2 : kPlanes) * kAtomBytes;
+  static constexpr int kOut = kGate + (int)sizeof(Gate) * kHeads * kGateSlots;  // state warps: outputs, ...
+  static constexpr int kDot = kOut + 8 * kOutBytes;                              // ... rows to multiply them with
+  static constexpr int kBar = kDot + 8 * kDotBytes;
+  static constexpr int kFlag = kBar + 8 * kBars;
+  static constexpr int kBytes = kFlag + 16 + 1024;                  // 1024: alignment of the base
+};
+
+__device__ __forceinline__ void tmem_ld8(uint32_t t, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
+      : "memory");
+}
+// 16 lanes x 32 columns in the layout of mma.sync's accumulators: registers 4 t .. 4 t + 3 are
+// columns 8 t + 2 (lane % 4), + 1 of row lane / 4, then of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256_x4(uint32_t t, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
+      : "memory");
+}
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t t, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t)
+               : "memory");
+}
+// 16 lanes x 32 columns: registers 2 t, 2 t + 1 are column 4 t + lane % 4 of rows lane / 4 and
+// lane / 4 + 8 (a pair of bf16 per column: the layout of 8 x 8 matrices from ldmatrix).
+__device__ __forceinline__ void tmem_st_16x128_x8(uint32_t t, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > limit) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// What every role needs.
+struct Cta {
+  uint8_t* smem;
+  uint64_t* bars;
+  volatile int* abort_flag;
+  long long limit;
+  uint32_t tmem;
+  int chunks;
+  int64_t t0;
+  int len, lane;
+  // A whole warp waits for the n-th completion of a barrier (n from 0).
+  __device__ __forceinline__ bool wait(int bar, int n) const {
+    const bool mine = mbar_try_wait(&bars[bar], (uint32_t)n & 1u) || wait_spin(&bars[bar], (uint32_t)n & 1u, abort_flag, limit);
+    return !__any_sync(0xffffffffu, !mine);
+  }
+  // A producer's wait for the slot's consumers; use number n (from 0) of the slot.
+  __device__ __forceinline__ bool wait_free(int bar, int n) const { return n == 0 || wait(bar, n - 1); }
+  // One arrival for the warp, after every lane's accesses.
+  __device__ __forceinline__ void arrive(int bar) const {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[bar]);
+  }
+  // The block processed at step c: its first token and its tokens.
+  __device__ __forceinline__ int64_t token(const LaPass& a, int c) const {
+    return t0 + (int64_t)(a.reverse ? chunks - 1 - c : c) * kC;
+  }
+  __device__ __forceinline__ int rows(const LaPass& a, int c) const {
+    return min(kC, len - (a.reverse ? chunks - 1 - c : c) * kC);
+  }
+};
+
+template <int NT, bool PAIR>
+__device__ __forceinline__ void load_role(const Cta& t, const LaPass& a, const CUtensorMap* tq, const CUtensorMap* tk,
+                          const CUtensorMap* tv, int h0) {
+  using L = TcSmem<NT, PAIR>;
+  const int qh = h0 / a.q_div, kh = h0 / a.k_div;
+  const int v_atoms = PAIR || a.PV > 64 ? 2 : 1;
+  const uint32_t bytes = ((a.states_only ? 1 : 2) * (NT / 64) + v_atoms) * kAtomBytes;
+  int c = 0;
+  for (; c < t.chunks; ++c) {
+    const int s = c % kStages;
+    if (!t.wait_free(kFree + s, c / kStages)) break;
+    if (t.lane == 0) {
+      uint64_t* bar = &t.bars[kFull + s];
+      uint8_t* base = t.smem + s * L::kStage;
+      const int tok = (int)t.token(a, c);
+      mbar_expect_tx(bar, bytes);
+#pragma unroll
+      for (int i = 0; i < NT / 64; ++i) tma_load_3d(base + L::kK + i * kAtomBytes, tk, 64 * i, kh, tok, bar);
+      for (int i = 0; i < v_atoms; ++i)
+        tma_load_3d(base + L::kV + i * kAtomBytes, tv, PAIR ? 0 : 64 * i, (PAIR ? h0 + i : h0) / a.v_div, tok, bar);
+      if (!a.states_only) {
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) tma_load_3d(base + L::kQ + i * kAtomBytes, tq, 64 * i, qh, tok, bar);
+      }
+    }
+    __syncwarp();
+  }
+  // after a failure: what was issued lands before the CTA ends
+  if (c < t.chunks)
+    for (int d = max(0, c - kStages); d < c; ++d)
+      mbar_wait_bounded(&t.bars[kFull + d % kStages], (uint32_t)(d / kStages) & 1u, 1ll << 32);
+}
+
+template <int NT, bool PAIR, int PL>
+__device__ __forceinline__ void mma_role(const Cta& t, const LaPass& a, int withhold) {
+  constexpr int planes = PL;
+  using L = TcSmem<NT, PAIR>;
+  const bool leader = elect_one();
+  const uint32_t base = smem_u32(t.smem);
+  const uint64_t k_major = sdesc_sw128(0, 16, 1024), mn_major = sdesc_sw128(0, kAtomBytes, 1024);
+  auto at = [&](uint64_t major, int off) { return major | (uint64_t)((base + off) >> 4); };
+  const uint32_t id_s1 = idesc_bf16(64, kC, 0, 0), id_yi = idesc_bf16(128, kC, 0, 0),
+                 id_ya = idesc_bf16(128, PAIR ? 2 * kC : kC, 1, 0), id_ds = idesc_bf16(128, NT, 0, 1);
+  constexpr int sp_slots = planes > 1 ? 2 : 1;
+  auto commit = [&](int bar) {
+    if (leader) umma_commit(&t.bars[bar]);
+    __syncwarp();
+  };
+  auto koff = [](int kk) { return (uint64_t)(((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4); };
+  auto s1 = [&](int c) -> bool {
+    const int s = c % kStages;
+    // the tiles as they landed: what a last block holds past its end is masked in P
+    if (!t.wait(kFull + s, c / kStages) || !t.wait_free(kS1Free, c)) return false;
+    tc_fence_after();
+    if (leader) {
+      const uint64_t q = at(k_major, s * L::kStage + L::kQ), k = at(k_major, s * L::kStage + L::kK);
+#pragma unroll 1
+      for (int kk = 0; kk < NT / 16; ++kk) umma_f16(t.tmem + kColS1, q + koff(kk), k + koff(kk), id_s1, kk > 0);
+    }
+    __syncwarp();
+    if (!withhold) commit(kS1Full);
+    return true;
+  };
+  bool ok = true;
+  if (!a.states_only && t.chunks) ok = s1(0);
+  for (int c = 0; ok && c < t.chunks; ++c) {
+    const int s = c % kStages;
+    if (!a.states_only) {
+      if (c + 1 < t.chunks && !(ok = s1(c + 1))) break;
+    }
+    // dS = (upd o value)^T key, plane by plane
+    if (!(ok = t.wait(kReady + s, c / kStages)) || !(ok = t.wait(kDsFree, c))) break;  // (the first time: S is loaded)
+    const uint64_t k_mn = at(mn_major, s * L::kStage + L::kK);
+#pragma unroll 1
+    for (int p = 0; p < kPlanes; ++p) {
+      const int m = kPlanes * c + p, slot = m & 1;
+      if (!(ok = t.wait(kUvFull + slot, m >> 1))) break;
+      tc_fence_after();
+      if (leader) {
+#pragma unroll 1
+        for (int kk = 0; kk < kC / 16; ++kk)
+          umma_f16_ta(t.tmem + kColDs, t.tmem + kColUv + slot * 32 + kk * 8, k_mn + kk * 128, id_ds, p > 0 || kk > 0);
+      }
+      __syncwarp();
+      commit(kUvFree + slot);
+    }
+    if (!ok) break;
+    commit(kDsFull);
+    if (a.states_only) {
+      commit(kFree + s);
+      continue;
+    }
+    // Yi^T = S query^T
+    if (!(ok = t.wait_free(kYFree, c))) break;
+    const uint64_t q = at(k_major, s * L::kStage + L::kQ);
+#pragma unroll 1
+    for (int p = 0; p < planes; ++p) {
+      const int m = planes * c + p, slot = m % sp_slots;
+      if (!(ok = t.wait(kSpFull + slot, m / sp_slots))) break;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t sp = t.tmem + (slot ? kColSp1 : kColSp0);
+#pragma unroll 1
+        for (int kk = 0; kk < NT / 16; ++kk)
+          umma_f16_ta(t.tmem + kColYi, sp + kk * 8, q + koff(kk), id_yi, p > 0 || kk > 0);
+      }
+      __syncwarp();
+      commit(kSpFree + slot);
+    }
+    if (!ok) break;
+    // Ya^T = value^T P^T
+    if (!(ok = t.wait(kPFull, c))) break;
+    tc_fence_after();
+    if (leader) {
+      const uint64_t v_mn = at(mn_major, s * L::kStage + L::kV);
+      for (int p = 0; p < planes; ++p) {
+        const uint64_t pm = at(k_major, L::kP + p * kAtomBytes);
+#pragma unroll 1
+        for (int kk = 0; kk < kC / 16; ++kk)
+          umma_f16(t.tmem + kColYa, v_mn + kk * 128, pm + kk * 2, id_ya, p > 0 || kk > 0);
+      }
+    }
+    __syncwarp();
+    commit(kPFree);
+    commit(kYFull);
+    commit(kFree + s);
+  }
+  commit(kDrain);
+  if (!mbar_wait_bounded(&t.bars[kDrain], 0, 1ll << 32)) *t.abort_flag = 1;
+}
+
+// One warp per head: lane l takes tokens 2 l and 2 l + 1 of each block.
+template <int NT, bool PAIR>
+__device__ __forceinline__ void gate_role(const Cta& t, const LaPass& a, int h, int which, int unit) {
+  using L = TcSmem<NT, PAIR>;
+  const int i0 = 2 * t.lane;
+  const float sr = a.reverse ? 1.f : a.scale, su = a.reverse ? a.scale : 1.f;
+  double total = 0.0;
+  auto load = [&](int c, float& x, float& y) {
+    x = y = 0.f;
+    if (c >= t.chunks) return;
+    const int64_t tok = t.token(a, c) + i0;
+    const int rows = t.rows(a, c);
+    if (i0 < rows) x = a.log_decay[a.per_token ? tok * a.H + h : h];
+    if (i0 + 1 < rows) y = a.log_decay[a.per_token ? (tok + 1) * a.H + h : h];
+  };
+  float x, y;
+  load(0, x, y);
+  for (int c = 0; c < t.chunks; ++c) {
+    const double l0 = log2_clamped(x), l1 = log2_clamped(y);
+    load(c + 1, x, y);
+    double c1 = l0 + l1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double v = __shfl_up_sync(0xffffffffu, c1, o);
+      if (t.lane >= o) c1 += v;
+    }
+    const double end = __shfl_sync(0xffffffffu, c1, 31), c0 = c1 - l1;
+    const int slot = c % kGateSlots;
+    if (!t.wait_free(kGFree + slot, c / kGateSlots)) return;
+    Gate* g = reinterpret_cast<Gate*>(t.smem + L::kGate) + slot * L::kHeads + which;
+    float hi[2], lo[2], row[2], upd[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const double cc = j ? c1 : c0, f = floor(cc), e = floor(end - cc);
+      hi[j] = (float)f, lo[j] = (float)(cc - f);
+      const float from_start = exp2_parts(hi[j], lo[j]), to_end = exp2_parts((float)e, (float)(end - cc - e));
+      row[j] = (a.reverse ? to_end : from_start) * sr;
+      upd[j] = (a.reverse ? from_start : to_end) * su;
+    }
+    *reinterpret_cast<float2*>(&g->chi[i0]) = make_float2(hi[0], hi[1]);
+    *reinterpret_cast<float2*>(&g->clo[i0]) = make_float2(lo[0], lo[1]);
+    *reinterpret_cast<float2*>(&g->row[i0]) = make_float2(row[0], row[1]);
+    *reinterpret_cast<float2*>(&g->upd[i0]) = make_float2(upd[0], upd[1]);
+    if (t.lane == 0) g->decay = exp2f((float)end);
+    total += end;
+    t.arrive(kGFull + slot);
+  }
+  if (a.states_only && t.lane == 0) a.window_decay[(int64_t)unit * a.H + h] = exp2_parts((float)floor(total), (float)(total - floor(total)));
+}
+
+// S1 -> P.  Warp q holds rows 16 q .. 16 q + 15 of S1 (lanes 0 .. 15 of its quarter of tensor
+// memory: a product of 64 rows puts 16 in each quarter).
+template <int NT, bool PAIR, int PL>
+__device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
+  constexpr int planes = PL;
+  using L = TcSmem<NT, PAIR>;
+  const int q = threadIdx.x / 32 & 3;
+  const int gr = t.lane >> 2, gc = (t.lane & 3) * 2;
+  const int i0 = 16 * q + gr;
+  uint8_t* P = t.smem + L::kP;
+  const int sign = a.reverse ? -1 : 1;
+  const float fsign = (float)sign;
+  auto put = [&](uint8_t* tile, int i, int j, uint32_t v) {
+    *reinterpret_cast<uint32_t*>(tile + sw128_off(i, j >> 3) + (j & 7) * 2) = v;
+  };
+  if (!a.states_only) {  // the tiles above the diagonal stay zero
+#pragma unroll 1
+    for (int n = 0; n < 8; ++n)
+#pragma unroll 1
+      for (int p = 0; p < (PAIR ? 2 : kPlanes); ++p) {
+        put(P + p * kAtomBytes, i0, 8 * n + gc, 0u);
+        put(P + p * kAtomBytes, i0 + 8, 8 * n + gc, 0u);
+      }
+  }
+  for (int c = 0; c < t.chunks; ++c) {
+    const int slot = c % kGateSlots;
+    if (!t.wait(kGFull + slot, c / kGateSlots)) return;
+    if (!a.states_only) {
+      const Gate* g = reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads;
+      if (!t.wait(kS1Full, c) || !t.wait_free(kPFree, c)) return;
+      tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {  // 32 columns at a time
+        uint32_t r[16];
+        tmem_ld_16x256_x4(t.tmem + ((uint32_t)(32 * q) << 16) + kColS1 + 32 * b, r);
+        tmem_ld_wait();
+        if (b) {
+          tc_fence_before();
+          t.arrive(kS1Free);
+        }
+#pragma unroll
+        for (int hh = 0; hh < L::kHeads; ++hh) {
+          const float hi0 = g[hh].chi[i0], hi1 = g[hh].chi[i0 + 8], lo0 = g[hh].clo[i0], lo1 = g[hh].clo[i0 + 8];
+#pragma unroll
+          for (int nn = 0; nn < 4; ++nn) {
+            const int n = 4 * b + nn, j = 8 * n + gc;
+            if (a.reverse ? n < 2 * q : n > 2 * q + 1) continue;
+            const float2 hj = *reinterpret_cast<const float2*>(&g[hh].chi[j]);
+            const float2 lj = *reinterpret_cast<const float2*>(&g[hh].clo[j]);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float dh = (e >> 1 ? hi1 : hi0) - (e & 1 ? hj.y : hj.x);
+              const float dl = (e >> 1 ? lo1 : lo0) - (e & 1 ? lj.y : lj.x);
+              const int ahead = i0 + 8 * (e >> 1) - j - (e & 1);  // i - j
+              v[e] = sign * ahead >= 0 ? __uint_as_float(r[4 * nn + e]) * ex2(fsign * (dh + dl)) * a.scale : 0.f;
+            }
+#pragma unroll
+            for (int p = 0; p < planes; ++p) {
+              const uint32_t x = bf16x2(v[0], v[1]), y = bf16x2(v[2], v[3]);
+              uint8_t* tile = P + (PAIR ? hh : p) * kAtomBytes;
+              put(tile, i0, j, x);
+              put(tile, i0 + 8, j, y);
+              v[0] -= bf16_lo(x), v[1] -= bf16_hi(x), v[2] -= bf16_lo(y), v[3] -= bf16_hi(y);
+            }
+          }
+        }
+      }
+      fence_proxy_async();
+      t.arrive(kPFull);
+    }
+    t.arrive(kGFree + slot);
+  }
+}
+
+// value -> the planes of upd o value in tensor memory, transposed on the way.  Warp q makes rows
+// 32 q .. 32 q + 31.
+template <int NT, bool PAIR>
+__device__ __forceinline__ void decay_role(const Cta& t, const LaPass& a) {
+  using L = TcSmem<NT, PAIR>;
+  const int q = threadIdx.x / 32 & 3, lane = t.lane;
+  const int head = PAIR ? q >> 1 : 0;
+  const bool active = (PAIR ? 32 * q & 63 : 32 * q) < a.PV;
+  for (int c = 0; c < t.chunks; ++c) {
+    const int s = c % kStages, slot = c % kGateSlots, rows = t.rows(a, c);
+    uint8_t* tiles = t.smem + s * L::kStage;
+    if (!t.wait(kFull + s, c / kStages)) return;
+    if (rows < kC) {
+      // the sequence ends inside the block: what follows is another's, and 0 * NaN is NaN
+      const int atoms = L::kStage / kAtomBytes - NT / 64;  // key and value
+      for (int e = threadIdx.x & 127; e < (kC - rows) * 8 * atoms; e += 128) {
+        const int at = e / ((kC - rows) * 8), x = e % ((kC - rows) * 8);
+        *reinterpret_cast<uint4*>(tiles + L::kK + at * kAtomBytes + (rows + x / 8) * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async();
+    }
+    t.arrive(kReady + s);
+    if (rows < kC && !t.wait(kReady + s, c / kStages)) return;
+    if (!t.wait(kGFull + slot, c / kGateSlots)) return;
+    const float* u = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads + head)->upd;
+    float x[2][16][2];
+    if (active) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const int j = 16 * kk + (lane & 7) + ((lane >> 4) & 1) * 8;
+        const float2 ua = *reinterpret_cast<const float2*>(&u[16 * kk + 2 * (lane & 3)]);
+        const float2 ub = *reinterpret_cast<const float2*>(&u[16 * kk + 8 + 2 * (lane & 3)]);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int p = 32 * q + 16 * hf + ((lane >> 3) & 1) * 8;
+          uint32_t v[4];
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(smem_u32(tiles + L::kV + (p >> 6) * kAtomBytes + sw128_off(j, (p & 63) >> 3)))
+                       : "memory");
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            x[hf][4 * kk + m][0] = bf16_lo(v[m]) * (m < 2 ? ua.x : ub.x);
+            x[hf][4 * kk + m][1] = bf16_hi(v[m]) * (m < 2 ? ua.y : ub.y);
+          }
+        }
+      }
+    }
+    t.arrive(kGFree + slot);
+#pragma unroll 1
+    for (int p = 0; p < kPlanes; ++p) {
+      const int m = kPlanes * c + p, us = m & 1;
+      if (!t.wait_free(kUvFree + us, m >> 1)) return;
+      tc_fence_after();
+      if (active) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            w[i] = bf16x2(x[hf][i][0], x[hf][i][1]);
+            x[hf][i][0] -= bf16_lo(w[i]), x[hf][i][1] -= bf16_hi(w[i]);
+          }
+          tmem_st_16x128_x8(t.tmem + ((uint32_t)(32 * q + 16 * hf) << 16) + kColUv + 32 * us, w);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      t.arrive(kUvFull + us);
+    }
+  }
+}
+
+// Writes the thread's part of the state, element n of its row to to[n * step]: through the columns
+// of dS in tensor memory (which no product uses at that time), so that a small loop does it.
+template <int NC>
+__device__ __forceinline__ void put_state(uint32_t ds, const float (&S)[NC], float* to, int64_t step, int count, bool mine) {
+#pragma unroll
+  for (int b = 0; b < NC / 16; ++b) {
+    uint32_t v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(S[16 * b + i]);
+    tmem_st16(ds + 16 * b, v);
+  }
+  tmem_st_wait();
+#pragma unroll 1
+  for (int n = 0; n < NC; n += 8) {
+    uint32_t v[8];
+    tmem_ld8(ds + n, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (mine && n + i < count) to[(n + i) * step] = __uint_as_float(v[i]);
+  }
+}
+
+// Plane p of the state that step c's outputs see, to tensor memory.
+template <int NT, int PL>
+__device__ __forceinline__ bool put_plane(const Cta& t, const float (&S)[NT / 2], bool active, uint32_t lanes, int half,
+                                          int c, int p) {
+  constexpr int NC = NT / 2, slots = PL > 1 ? 2 : 1;
+  const int m = PL * c + p, slot = m % slots;
+  if (!t.wait_free(kSpFree + slot, m / slots)) return false;
+  tc_fence_after();
+  if (active) {
+    const uint32_t to = t.tmem + lanes + (slot ? kColSp1 : kColSp0) + half * (NC / 2);
+#pragma unroll
+    for (int b = 0; b < NC / 32; ++b) {
+      uint32_t v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float x = S[32 * b + 2 * i], y = S[32 * b + 2 * i + 1];
+        v[i] = bf16x2(x, y);
+#pragma unroll
+        for (int k = 0; k < PL - 1; ++k) {
+          if (k >= p) break;
+          x -= bf16_lo(v[i]), y -= bf16_hi(v[i]);
+          v[i] = bf16x2(x, y);
+        }
+      }
+      tmem_st16(to + 16 * b, v);
+    }
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  t.arrive(kSpFull + slot);
+  return true;
+}
+
+// S in registers: warp w (of 8) holds rows 32 (w % 4) .. and half of the columns; of the outputs
+// it writes the same rows and half of the block's tokens.
+template <int NT, bool PAIR, int PL>
+__device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const Unit& un, int u, int h0) {
+  constexpr int planes = PL;
+  using L = TcSmem<NT, PAIR>;
+  constexpr int NC = NT / 2;  // columns of a thread
+  const int w = threadIdx.x / 32 - kStateWarp, q = w & 3, half = w >> 2;
+  const int head = PAIR ? q >> 1 : 0, h = h0 + head;
+  const int r = PAIR ? (32 * q & 63) + t.lane : 32 * q + t.lane;  // value row of the head
+  const bool active = r - t.lane < a.PV, mine = r < a.PV;
+  const int n0 = half * NC;
+  const bool begins = a.reverse ? un.last : un.first, ends = a.reverse ? un.first : un.last;
+  const uint32_t lanes = (uint32_t)(32 * q) << 16;
+  const int64_t state_at = ((int64_t)un.seq * a.H + h) * a.NK * a.PV;
+  constexpr int sp_slots = planes > 1 ? 2 : 1;
+  const uint32_t ds = t.tmem + lanes + kColDs + n0;  // the thread's part of dS
+  const int count = max(0, min(NC, a.NK - n0));
+  auto window_at = [&](float* base, int64_t win) { return base + ((win * a.H + h) * a.PV + r) * a.NK + n0; };
+  float S[NC];
+  {
+    const float* from = nullptr;
+    int64_t step = 1;
+    if (begins) {
+      if (a.start) from = a.start + state_at + r * a.sr + n0 * a.sc, step = a.sc;
+    } else if (!a.states_only) {
+      from = window_at(a.carry, u);
+    }
+#pragma unroll 1
+    for (int n = 0; n < NC; n += 8) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = from && mine && n + i < count ? __float_as_uint(from[(n + i) * step]) : 0u;
+      tmem_st8(ds + n, v);
+    }
+    tmem_st_wait();
+#pragma unroll
+    for (int b = 0; b < NC / 16; ++b) {
+      uint32_t v[16];
+      tmem_ld16(ds + 16 * b, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) S[16 * b + i] = __uint_as_float(v[i]);
+    }
+  }
+  // Outputs of step c: the warp's 32 rows, tokens 32 half .. 32 half + 31 of the block, 16 at a
+  // time.  Tensor memory is read in the layout of mma.sync's accumulators (registers are pairs of
+  // tokens of one row), turned by transposing stores to shared memory, and written from there
+  // in 16-byte pieces (single 2-byte stores took 16 cycles each, 5 of a block's 9 thousand).
+  uint8_t* stage = t.smem + L::kOut + w * kOutBytes;
+  uint8_t* dots_in = t.smem + L::kDot + w * kDotBytes;
+  const int row0 = r - t.lane;  // the warp's first row of the head
+  auto outputs = [&](int c) -> bool {
+    const float* rowf = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (c % kGateSlots) * L::kHeads + head)->row + 32 * half;
+    if (!t.wait(kYFull, c)) return false;
+    tc_fence_after();
+    const int64_t tok = t.token(a, c) + 32 * half;
+    const int rows = t.rows(a, c) - 32 * half;
+    const int64_t pitch = (int64_t)a.H * a.PV, at = tok * pitch + (int64_t)h * a.PV + row0;
+    const int gr = t.lane >> 2, gc = (t.lane & 3) * 2;
+    if constexpr (PL > 1) {
+      cp_async_wait_all();
+      __syncwarp();
+    }
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+      uint32_t yi[2][8], ya[2][8];
+      if (active) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t from = t.tmem + lanes + ((uint32_t)(16 * hf) << 16) + 32 * half + 16 * b;
+          tmem_ld_16x256_x2(from + kColYi, yi[hf]);
+          tmem_ld_16x256_x2(from + kColYa + (PAIR ? kC * head : 0), ya[hf]);
+        }
+        tmem_ld_wait();
+      }
+      if (b) {
+        tc_fence_before();
+        t.arrive(kYFree);
+      }
+      if (!active) continue;
+      const float2 f0 = *reinterpret_cast<const float2*>(&rowf[16 * b + gc]);
+      const float2 f1 = *reinterpret_cast<const float2*>(&rowf[16 * b + 8 + gc]);
+      float o[2][8];  // [half of the rows][4 tile of 8 tokens + 2 (row + 8) + token of the pair]
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          o[hf][e] = fmaf(__uint_as_float(yi[hf][e]), e < 4 ? (e & 1 ? f0.y : f0.x) : (e & 1 ? f1.y : f1.x),
+                          __uint_as_float(ya[hf][e]));
+      if (a.out_f32) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float*>(stage + (8 * (e >> 2) + gc + (e & 1)) * kOutPitch32 +
+                                      (16 * hf + 8 * ((e >> 1) & 1) + gr) * 4) = o[hf][e];
+        __syncwarp();
+        float* to = static_cast<float*>(a.out) + at + 16 * b * pitch;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = 4 * k + (t.lane >> 3), p = (t.lane & 7) * 4;
+          const float4 v = *reinterpret_cast<const float4*>(stage + i * kOutPitch32 + p * 4);
+          if (16 * b + i < rows && row0 + p < a.PV) *reinterpret_cast<float4*>(to + i * pitch + p) = v;
+        }
+      } else {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint8_t* to = stage + (8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf + 16 * ((t.lane >> 3) & 1);
+          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(to)),
+                       "r"(bf16x2(o[hf][0], o[hf][1])), "r"(bf16x2(o[hf][2], o[hf][3])),
+                       "r"(bf16x2(o[hf][4], o[hf][5])), "r"(bf16x2(o[hf][6], o[hf][7]))
+                       : "memory");
+        }
+        __syncwarp();
+        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at + 16 * b * pitch;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = 8 * k + gr, p = (t.lane & 3) * 8;
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + i * kOutPitch + p * 2);
+          if (16 * b + i < rows && row0 + p < a.PV) *reinterpret_cast<uint4*>(to + i * pitch + p) = v;
+        }
+      }
+      __syncwarp();
+      if constexpr (PL > 1) {  // sums over the warp's rows of out * dot, for the decay's gradient
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t v[4];
+          const uint8_t* from = dots_in + (16 * b + 8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf + 16 * ((t.lane >> 3) & 1);
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(smem_u32(from))
+                       : "memory");
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            sum[2 * (m >> 1)] = fmaf(o[hf][2 * m], bf16_lo(v[m]), sum[2 * (m >> 1)]);
+            sum[2 * (m >> 1) + 1] = fmaf(o[hf][2 * m + 1], bf16_hi(v[m]), sum[2 * (m >> 1) + 1]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 4);
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 8);
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
+        }
+        // lanes 0 .. 3 have tokens gc, gc + 1, gc + 8, gc + 9; lane 4 m + l writes the m-th
+        const int m = t.lane >> 2, i = 16 * b + gc + (m & 1) + 8 * (m >> 1);
+        if (m < 4 && i < rows)
+          a.dots[((int64_t)q * a.tokens + tok + i) * a.H + h] = m == 0 ? sum[0] : m == 1 ? sum[1] : m == 2 ? sum[2] : sum[3];
+      }
+    }
+    t.arrive(kGFree + c % kGateSlots);
+    return true;
+  };
+  // The rows that step c's outputs are multiplied with, on their way while S is updated.
+  auto fetch_dots = [&](int c) {
+    const int64_t tok = t.token(a, c) + 32 * half;
+    const int rows = t.rows(a, c) - 32 * half;
+    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.dot) + (tok * a.dot_heads + h / a.dot_div) * a.PV + row0;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      const int i = 8 * k + (t.lane >> 2), p = (t.lane & 3) * 8;
+      const bool in = i < rows && row0 + p < a.PV;
+      const void* src = in ? from + (int64_t)i * a.dot_heads * a.PV + p : static_cast<const __nv_bfloat16*>(a.dot);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dots_in + i * kOutPitch + p * 2)),
+                   "l"(src), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+    cp_async_commit();
+  };
+
+  constexpr int early = planes < sp_slots ? planes : sp_slots;
+  // windows whose state is wanted: forward, after the window's last block; reverse, before it
+  auto wanted = [&](int ci) { return a.dump && (ci == t.chunks - 1 || (ci + 1) * kC % a.window == 0); };
+  auto dump_at = [&](int ci) { return window_at(a.dump, un.first_window + ci * kC / a.window); };
+  if (a.reverse && t.chunks && wanted(t.chunks - 1)) put_state<NC>(ds, S, dump_at(t.chunks - 1), 1, count, mine);
+  tc_fence_before();
+  t.arrive(kDsFree);
+  if (!a.states_only && t.chunks)
+#pragma unroll
+    for (int p = 0; p < planes; ++p)
+      if (!put_plane<NT, PL>(t, S, active, lanes, half, 0, p)) return;
+  for (int c = 0; c < t.chunks; ++c) {
+    const int ci = a.reverse ? t.chunks - 1 - c : c;
+    if constexpr (PL > 1) fetch_dots(c);
+    if (!t.wait(kGFull + c % kGateSlots, c / kGateSlots)) return;
+    const float dec = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (c % kGateSlots) * L::kHeads + head)->decay;
+    if (!t.wait(kDsFull, c)) return;
+    tc_fence_after();
+#pragma unroll
+    for (int b = 0; b < NC / 16; ++b) {
+      uint32_t d[16];
+      tmem_ld16(ds + 16 * b, d);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(S[16 * b + i], dec, __uint_as_float(d[i]));
+    }
+    const int at = a.reverse ? ci - 1 : ci;  // the block whose window's state this may be
+    if (at >= 0 && wanted(at)) put_state<NC>(ds, S, dump_at(at), 1, count, mine);
+    tc_fence_before();
+    t.arrive(kDsFree);
+    if (a.states_only) {
+      t.arrive(kGFree + c % kGateSlots);
+      continue;
+    }
+    // The next step's planes go out before this step's outputs, as far as their slots do not
+    // wait for the products behind those outputs.
+    const bool more = c + 1 < t.chunks;
+#pragma unroll
+    for (int p = 0; p < planes; ++p) {
+      if (p == early && !outputs(c)) return;
+      if (more && !put_plane<NT, PL>(t, S, active, lanes, half, c + 1, p)) return;
+    }
+    if (early == planes && !outputs(c)) return;
+  }
+  if (a.states_only)
+    put_state<NC>(ds, S, window_at(a.carry, u), 1, count, mine);
+  else if (a.last && ends)
+    put_state<NC>(ds, S, a.last + state_at + r * a.sr + n0 * a.sc, a.sc, count, mine);
+}
+
+// Grid: units x heads (or pairs of heads), heads fastest.
+template <int NT, bool PAIR, int PL>
+__global__ void __launch_bounds__(kThreadsTc, 1)
+    la_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ LaPass a, unsigned int* status, long long limit, int withhold) {
+  using L = TcSmem<NT, PAIR>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  const int lanes_of_heads = PAIR ? a.H / 2 : a.H;
+  const int u = blockIdx.x / lanes_of_heads, h0 = (blockIdx.x % lanes_of_heads) * L::kHeads;
+  Unit un;
+  if (!get_unit(a, u, un)) return;
+  if (a.states_only && (a.reverse ? un.first : un.last)) return;  // nothing follows this window
+  const int warp = threadIdx.x >> 5;
+  Cta t;
+  t.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  t.bars = reinterpret_cast<uint64_t*>(t.smem + L::kBar);
+  t.abort_flag = reinterpret_cast<volatile int*>(t.smem + L::kFlag);
+  t.limit = limit;
+  t.lane = threadIdx.x & 31;
+  t.t0 = un.t0, t.len = un.len;
+  t.chunks = (un.len + kC - 1) / kC;
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, kTmem);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBars; ++i) {
+      int n = 1;
+      if (i >= kReady && i < kFree) n = 4;
+      if (i == kS1Free || i == kPFull || (i >= kUvFull && i < kUvFree)) n = 4;
+      if (i == kDsFree || i == kYFree || (i >= kSpFull && i < kSpFree)) n = 8;
+      if (i >= kGFull && i < kGFree) n = L::kHeads;
+      if (i >= kGFree && i < kDrain) n = 16;
+      mbar_init(&t.bars[i], n);
+    }
+    *t.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tensormap(&tq);
+    prefetch_tensormap(&tk);
+    prefetch_tensormap(&tv);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  t.tmem = s_tmem;
+
+  // Registers: 640 threads start with 96 each (61440); the warpgroups' shares after the split,
+  // 128 x (40 + 72 + 104 + 2 x 128) = 60416, fit what the launch holds.
+  if (warp < kMaskWarp) {
+    set_regs_dec<40>();
+    if (warp == kLoadWarp)
+      load_role<NT, PAIR>(t, a, &tq, &tk, &tv, h0);
+    else if (warp == kMmaWarp)
+      mma_role<NT, PAIR, PL>(t, a, withhold);
+    else if (warp - kGateWarp < L::kHeads)
+      gate_role<NT, PAIR>(t, a, h0 + warp - kGateWarp, warp - kGateWarp, u);
+  } else if (warp < kDecayWarp) {
+    set_regs_dec<72>();
+    mask_role<NT, PAIR, PL>(t, a);
+  } else if (warp < kStateWarp) {
+    set_regs_inc<104>();
+    decay_role<NT, PAIR>(t, a);
+  } else {
+    set_regs_inc<128>();
+    state_role<NT, PAIR, PL>(t, a, un, u, h0);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *t.abort_flag) atomicOr(status, kStatusTimeout);
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(s_tmem, kTmem);
+  }
+}
+
+// {dim, heads, tokens} with boxes of 64 columns of one head and 64 tokens, 128-byte swizzle;
+// what lies past the head's columns or the last token reads as zero.
+bool make_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t tokens) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)dim * heads * 2};
+  cuuint32_t box[3] = {64, 1, kC}, one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, bool PAIR, int PL>
+cudaError_t launch_one(const LaPass& p, cudaStream_t st) {
+  auto* fn = la_tc_kernel<NT, PAIR, PL>;
+  using L = TcSmem<NT, PAIR>;
+  static_assert(L::kBytes <= 227 * 1024, "tiles must fit the SM's shared memory");
+  CUtensorMap tq, tk, tv;
+  if (!make_map(&tq, p.query, p.NK, p.q_heads, p.tokens) || !make_map(&tk, p.key, p.NK, p.k_heads, p.tokens) ||
+      !make_map(&tv, p.value, p.PV, p.v_heads, p.tokens))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t units = p.segmented ? p.max_windows : p.nseq;
+  fn<<<(unsigned)(units * (PAIR ? p.H / 2 : p.H)), kThreadsTc, L::kBytes, st>>>(
+      tq, tk, tv, p, device_status_word(), device_wait_limit(), device_withhold() & 4);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool la_tc_supports(const LaPass& p) { return p.tokens > 0 && p.NK % 8 == 0 && p.PV % 8 == 0; }
+
+bool la_tc_pairs(const LaPass& p) {
+  return p.PV <= 64 && p.H % 2 == 0 && p.q_div % 2 == 0 && p.k_div % 2 == 0 && p.v_div == 1;
+}
+
+cudaError_t launch_la_tc(const LaPass& p, bool exact, cudaStream_t st) {
+  const bool narrow = p.NK <= 64;
+  if (exact) return narrow ? launch_one<64, false, kPlanes>(p, st) : launch_one<128, false, kPlanes>(p, st);
+  if (la_tc_pairs(p)) return narrow ? launch_one<64, true, 1>(p, st) : launch_one<128, true, 1>(p, st);
+  return narrow ? launch_one<64, false, 1>(p, st) : launch_one<128, false, 1>(p, st);
+}
+
+}  // namespace ssd
