@@ -15,18 +15,19 @@
 // runs while the previous one finishes.
 //
 // One CTA per SM takes one head (up to 128 value rows), or two heads of up to 64 rows each
-// that share query and key, and walks the blocks of its unit.  20 warps, each with one task, so
+// that share query and key, and walks the blocks of its unit.  28 warps, each with one task, so
 // that the tasks of several blocks overlap without any of them being interleaved by hand:
 //   load  (1 warp)   query, key, value tiles by TMA, three stages
 //   mma   (1 warp)   issues every product
 //   gates (2 warps)  a head each: the sums of log-decays in 64 bits and the factors from them
 //   mask  (4 warps)  S1 -> P
-//   decay (4 warps)  value -> the planes of upd o value, by transposing loads
-//   state (8 warps)  dS -> S -> the bf16 planes of S; Yi, Ya -> out
-// Tensor memory (512 columns): S1 64, Yi 64, Ya 64 (two heads 128), dS 128, planes of
-// upd o value 2 x 32, planes of S 64 (`planes` = 3: 2 x 64).
+//   decay (8 warps)  value -> the planes of upd o value, by transposing loads
+//   state (8 warps)  dS -> S -> the bf16 planes of S
+//   out   (4 warps)  Yi, Ya -> out
+// Tensor memory (512 columns): S1 64, Yi 64, Ya 64, dS 128, planes of upd o value 2 x 32, planes
+// of S 2 x 64 (two heads: Ya 128, S 64).
 //
-// With planes = 3 P and S enter their products as three bf16 planes each (fp32 accuracy), which
+// With PL = 3 P and S enter their products as three bf16 planes each (fp32 accuracy), which
 // the per-token dot products behind the decay's gradient need.
 //
 // Every wait is bounded; one that runs out stops the CTA's roles, which drain what is in
@@ -50,9 +51,9 @@ using namespace sm100;
 
 constexpr int kC = kLaChunk;  // tokens of a block
 constexpr int kAtomBytes = kC * 128;  // 64 tokens x 64 columns of bf16, 128-byte rows
-constexpr int kStages = 3, kGateSlots = 4, kPlanes = 3;
-constexpr int kWarpsTc = 20, kThreadsTc = 32 * kWarpsTc;
-constexpr int kLoadWarp = 0, kMmaWarp = 1, kGateWarp = 2, kMaskWarp = 4, kDecayWarp = 8, kStateWarp = 12;
+constexpr int kMaxStages = 3, kGateSlots = 4, kPlanes = 3;
+constexpr int kWarpsTc = 28, kThreadsTc = 32 * kWarpsTc;
+constexpr int kLoadWarp = 0, kMmaWarp = 1, kGateWarp = 2, kMaskWarp = 4, kDecayWarp = 8, kStateWarp = 16, kOutWarp = 24;
 
 // tensor memory columns
 constexpr int kColS1 = 0, kColYi = 64, kColYa = 128, kColDs = 256, kColUv = 384, kColSp0 = 448, kColSp1 = 192;
@@ -60,11 +61,11 @@ constexpr int kTmem = 512;
 
 enum Bar {
   kFull = 0,                     // tiles of a stage have landed
-  kReady = kFull + kStages,      // ... and rows past the sequence's end are zero (decay warps)
-  kFree = kReady + kStages,      // every product that reads the stage is done
-  kS1Full = kFree + kStages, kS1Free,
-  kPFull, kPFree,
-  kUvFull, kUvFree = kUvFull + 2,
+  kReady = kFull + kMaxStages,   // ... and rows past the sequence's end are zero (decay warps)
+  kFree = kReady + kMaxStages,      // every product that reads the stage is done
+  kS1Full = kFree + kMaxStages, kS1Free,
+  kPFull, kPFree = kPFull + 2,
+  kUvFull = kPFree + 2, kUvFree = kUvFull + 2,
   kDsFull = kUvFree + 2, kDsFree,
   kSpFull, kSpFree = kSpFull + 2,
   kYFull = kSpFree + 2, kYFree,
@@ -78,19 +79,21 @@ struct Gate {
   float decay, pad[3];
 };
 
-// A state warp's own staging: 16 tokens x 32 rows of outputs (bf16: 80 bytes a token, fp32: 144;
-// neither pitch has bank conflicts), and 32 tokens x 32 rows of bf16.
-constexpr int kOutBytes = 16 * 144, kOutPitch = 80, kOutPitch32 = 144, kDotBytes = 32 * kOutPitch;
+// An output warp's own staging: 16 tokens x 32 rows of outputs (bf16: 80 bytes a token, fp32: 144;
+// neither pitch has bank conflicts), and 64 tokens x 32 rows of bf16.
+constexpr int kOutBytes = 16 * 144, kOutPitch = 80, kOutPitch32 = 144, kDotBytes = kC * kOutPitch;
 
-template <int NT, bool PAIR>
+template <int NT, bool PAIR, int PL>
 struct TcSmem {
+  static constexpr int kStages = PL > 1 ? 2 : 3;   // (three planes of P leave room for two)
+  static constexpr int kPTiles = PAIR ? 2 : PL;    // tiles of P: planes, or one per head
   static constexpr int kHeads = PAIR ? 2 : 1;
   static constexpr int kQ = 0, kK = NT / 64 * kAtomBytes, kV = 2 * kK, kStage = kV + 2 * kAtomBytes;
-  static constexpr int kP = kStages * kStage;                       // P: planes, or one per head
-  static constexpr int kGate = kP + (PAIR ? 2 : kPlanes) * kAtomBytes;
-  static constexpr int kOut = kGate + (int)sizeof(Gate) * kHeads * kGateSlots;  // state warps: outputs, ...
-  static constexpr int kDot = kOut + 8 * kOutBytes;                              // ... rows to multiply them with
-  static constexpr int kBar = kDot + 8 * kDotBytes;
+  static constexpr int kP = kStages * kStage;      // P: two buffers
+  static constexpr int kGate = kP + 2 * kPTiles * kAtomBytes;
+  static constexpr int kOut = kGate + (int)sizeof(Gate) * kHeads * kGateSlots;  // out warps: staged outputs, ...
+  static constexpr int kDot = kOut + 4 * kOutBytes;                              // ... rows to multiply them with
+  static constexpr int kBar = kDot + 4 * kDotBytes;
   static constexpr int kFlag = kBar + 8 * kBars;
   static constexpr int kBytes = kFlag + 16 + 1024;                  // 1024: alignment of the base
 };
@@ -133,15 +136,12 @@ __device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t t, uint32_t (&r)[8]) 
                : "r"(t)
                : "memory");
 }
-// 16 lanes x 32 columns: registers 2 t, 2 t + 1 are column 4 t + lane % 4 of rows lane / 4 and
+// 16 lanes x 16 columns: registers 2 t, 2 t + 1 are column 4 t + lane % 4 of rows lane / 4 and
 // lane / 4 + 8 (a pair of bf16 per column: the layout of 8 x 8 matrices from ldmatrix).
-__device__ __forceinline__ void tmem_st_16x128_x8(uint32_t t, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st_16x128_x4(uint32_t t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 template <int N>
@@ -196,17 +196,17 @@ struct Cta {
   }
 };
 
-template <int NT, bool PAIR>
+template <int NT, bool PAIR, int PL>
 __device__ __forceinline__ void load_role(const Cta& t, const LaPass& a, const CUtensorMap* tq, const CUtensorMap* tk,
                           const CUtensorMap* tv, int h0) {
-  using L = TcSmem<NT, PAIR>;
+  using L = TcSmem<NT, PAIR, PL>;
   const int qh = h0 / a.q_div, kh = h0 / a.k_div;
   const int v_atoms = PAIR || a.PV > 64 ? 2 : 1;
   const uint32_t bytes = ((a.states_only ? 1 : 2) * (NT / 64) + v_atoms) * kAtomBytes;
   int c = 0;
   for (; c < t.chunks; ++c) {
-    const int s = c % kStages;
-    if (!t.wait_free(kFree + s, c / kStages)) break;
+    const int s = c % L::kStages;
+    if (!t.wait_free(kFree + s, c / L::kStages)) break;
     if (t.lane == 0) {
       uint64_t* bar = &t.bars[kFull + s];
       uint8_t* base = t.smem + s * L::kStage;
@@ -225,30 +225,30 @@ __device__ __forceinline__ void load_role(const Cta& t, const LaPass& a, const C
   }
   // after a failure: what was issued lands before the CTA ends
   if (c < t.chunks)
-    for (int d = max(0, c - kStages); d < c; ++d)
-      mbar_wait_bounded(&t.bars[kFull + d % kStages], (uint32_t)(d / kStages) & 1u, 1ll << 32);
+    for (int d = max(0, c - L::kStages); d < c; ++d)
+      mbar_wait_bounded(&t.bars[kFull + d % L::kStages], (uint32_t)(d / L::kStages) & 1u, 1ll << 32);
 }
 
 template <int NT, bool PAIR, int PL>
 __device__ __forceinline__ void mma_role(const Cta& t, const LaPass& a, int withhold) {
   constexpr int planes = PL;
-  using L = TcSmem<NT, PAIR>;
+  using L = TcSmem<NT, PAIR, PL>;
   const bool leader = elect_one();
   const uint32_t base = smem_u32(t.smem);
   const uint64_t k_major = sdesc_sw128(0, 16, 1024), mn_major = sdesc_sw128(0, kAtomBytes, 1024);
   auto at = [&](uint64_t major, int off) { return major | (uint64_t)((base + off) >> 4); };
   const uint32_t id_s1 = idesc_bf16(64, kC, 0, 0), id_yi = idesc_bf16(128, kC, 0, 0),
                  id_ya = idesc_bf16(128, PAIR ? 2 * kC : kC, 1, 0), id_ds = idesc_bf16(128, NT, 0, 1);
-  constexpr int sp_slots = planes > 1 ? 2 : 1;
+  constexpr int sp_slots = PAIR ? 1 : 2;
   auto commit = [&](int bar) {
     if (leader) umma_commit(&t.bars[bar]);
     __syncwarp();
   };
   auto koff = [](int kk) { return (uint64_t)(((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4); };
   auto s1 = [&](int c) -> bool {
-    const int s = c % kStages;
+    const int s = c % L::kStages;
     // the tiles as they landed: what a last block holds past its end is masked in P
-    if (!t.wait(kFull + s, c / kStages) || !t.wait_free(kS1Free, c)) return false;
+    if (!t.wait(kFull + s, c / L::kStages) || !t.wait_free(kS1Free, c)) return false;
     tc_fence_after();
     if (leader) {
       const uint64_t q = at(k_major, s * L::kStage + L::kQ), k = at(k_major, s * L::kStage + L::kK);
@@ -262,12 +262,12 @@ __device__ __forceinline__ void mma_role(const Cta& t, const LaPass& a, int with
   bool ok = true;
   if (!a.states_only && t.chunks) ok = s1(0);
   for (int c = 0; ok && c < t.chunks; ++c) {
-    const int s = c % kStages;
+    const int s = c % L::kStages;
     if (!a.states_only) {
       if (c + 1 < t.chunks && !(ok = s1(c + 1))) break;
     }
     // dS = (upd o value)^T key, plane by plane
-    if (!(ok = t.wait(kReady + s, c / kStages)) || !(ok = t.wait(kDsFree, c))) break;  // (the first time: S is loaded)
+    if (!(ok = t.wait(kReady + s, c / L::kStages)) || !(ok = t.wait(kDsFree, c))) break;  // (the first time: S is loaded)
     const uint64_t k_mn = at(mn_major, s * L::kStage + L::kK);
 #pragma unroll 1
     for (int p = 0; p < kPlanes; ++p) {
@@ -307,19 +307,19 @@ __device__ __forceinline__ void mma_role(const Cta& t, const LaPass& a, int with
     }
     if (!ok) break;
     // Ya^T = value^T P^T
-    if (!(ok = t.wait(kPFull, c))) break;
+    if (!(ok = t.wait(kPFull + (c & 1), c >> 1))) break;
     tc_fence_after();
     if (leader) {
       const uint64_t v_mn = at(mn_major, s * L::kStage + L::kV);
       for (int p = 0; p < planes; ++p) {
-        const uint64_t pm = at(k_major, L::kP + p * kAtomBytes);
+        const uint64_t pm = at(k_major, L::kP + ((c & 1) * L::kPTiles + p) * kAtomBytes);
 #pragma unroll 1
         for (int kk = 0; kk < kC / 16; ++kk)
           umma_f16(t.tmem + kColYa, v_mn + kk * 128, pm + kk * 2, id_ya, p > 0 || kk > 0);
       }
     }
     __syncwarp();
-    commit(kPFree);
+    commit(kPFree + (c & 1));
     commit(kYFull);
     commit(kFree + s);
   }
@@ -328,9 +328,9 @@ __device__ __forceinline__ void mma_role(const Cta& t, const LaPass& a, int with
 }
 
 // One warp per head: lane l takes tokens 2 l and 2 l + 1 of each block.
-template <int NT, bool PAIR>
+template <int NT, bool PAIR, int PL>
 __device__ __forceinline__ void gate_role(const Cta& t, const LaPass& a, int h, int which, int unit) {
-  using L = TcSmem<NT, PAIR>;
+  using L = TcSmem<NT, PAIR, PL>;
   const int i0 = 2 * t.lane;
   const float sr = a.reverse ? 1.f : a.scale, su = a.reverse ? a.scale : 1.f;
   double total = 0.0;
@@ -382,7 +382,7 @@ __device__ __forceinline__ void gate_role(const Cta& t, const LaPass& a, int h, 
 template <int NT, bool PAIR, int PL>
 __device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
   constexpr int planes = PL;
-  using L = TcSmem<NT, PAIR>;
+  using L = TcSmem<NT, PAIR, PL>;
   const int q = threadIdx.x / 32 & 3;
   const int gr = t.lane >> 2, gc = (t.lane & 3) * 2;
   const int i0 = 16 * q + gr;
@@ -396,7 +396,7 @@ __device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
 #pragma unroll 1
     for (int n = 0; n < 8; ++n)
 #pragma unroll 1
-      for (int p = 0; p < (PAIR ? 2 : kPlanes); ++p) {
+      for (int p = 0; p < 2 * L::kPTiles; ++p) {
         put(P + p * kAtomBytes, i0, 8 * n + gc, 0u);
         put(P + p * kAtomBytes, i0 + 8, 8 * n + gc, 0u);
       }
@@ -406,7 +406,7 @@ __device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
     if (!t.wait(kGFull + slot, c / kGateSlots)) return;
     if (!a.states_only) {
       const Gate* g = reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads;
-      if (!t.wait(kS1Full, c) || !t.wait_free(kPFree, c)) return;
+      if (!t.wait(kS1Full, c) || !t.wait_free(kPFree + (c & 1), c >> 1)) return;
       tc_fence_after();
 #pragma unroll 1
       for (int b = 0; b < 2; ++b) {  // 32 columns at a time
@@ -437,7 +437,7 @@ __device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
 #pragma unroll
             for (int p = 0; p < planes; ++p) {
               const uint32_t x = bf16x2(v[0], v[1]), y = bf16x2(v[2], v[3]);
-              uint8_t* tile = P + (PAIR ? hh : p) * kAtomBytes;
+              uint8_t* tile = P + ((c & 1) * L::kPTiles + (PAIR ? hh : p)) * kAtomBytes;
               put(tile, i0, j, x);
               put(tile, i0 + 8, j, y);
               v[0] -= bf16_lo(x), v[1] -= bf16_hi(x), v[2] -= bf16_lo(y), v[3] -= bf16_hi(y);
@@ -446,42 +446,42 @@ __device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
         }
       }
       fence_proxy_async();
-      t.arrive(kPFull);
+      t.arrive(kPFull + (c & 1));
     }
     t.arrive(kGFree + slot);
   }
 }
 
-// value -> the planes of upd o value in tensor memory, transposed on the way.  Warp q makes rows
-// 32 q .. 32 q + 31.
-template <int NT, bool PAIR>
+// value -> the planes of upd o value in tensor memory, transposed on the way.  Warp w makes rows
+// 32 (w % 4) .. and half of the block's tokens.
+template <int NT, bool PAIR, int PL>
 __device__ __forceinline__ void decay_role(const Cta& t, const LaPass& a) {
-  using L = TcSmem<NT, PAIR>;
-  const int q = threadIdx.x / 32 & 3, lane = t.lane;
+  using L = TcSmem<NT, PAIR, PL>;
+  const int w = threadIdx.x / 32 - kDecayWarp, q = w & 3, half = w >> 2, lane = t.lane;
   const int head = PAIR ? q >> 1 : 0;
   const bool active = (PAIR ? 32 * q & 63 : 32 * q) < a.PV;
   for (int c = 0; c < t.chunks; ++c) {
-    const int s = c % kStages, slot = c % kGateSlots, rows = t.rows(a, c);
+    const int s = c % L::kStages, slot = c % kGateSlots, rows = t.rows(a, c);
     uint8_t* tiles = t.smem + s * L::kStage;
-    if (!t.wait(kFull + s, c / kStages)) return;
+    if (!t.wait(kFull + s, c / L::kStages)) return;
     if (rows < kC) {
       // the sequence ends inside the block: what follows is another's, and 0 * NaN is NaN
       const int atoms = L::kStage / kAtomBytes - NT / 64;  // key and value
-      for (int e = threadIdx.x & 127; e < (kC - rows) * 8 * atoms; e += 128) {
+      for (int e = threadIdx.x & 255; e < (kC - rows) * 8 * atoms; e += 256) {
         const int at = e / ((kC - rows) * 8), x = e % ((kC - rows) * 8);
         *reinterpret_cast<uint4*>(tiles + L::kK + at * kAtomBytes + (rows + x / 8) * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async();
     }
     t.arrive(kReady + s);
-    if (rows < kC && !t.wait(kReady + s, c / kStages)) return;
+    if (rows < kC && !t.wait(kReady + s, c / L::kStages)) return;
     if (!t.wait(kGFull + slot, c / kGateSlots)) return;
-    const float* u = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads + head)->upd;
-    float x[2][16][2];
+    const float* u = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads + head)->upd + 32 * half;
+    float x[2][8][2];  // [half of the rows][4 k step of 16 tokens + matrix][token of the pair]
     if (active) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const int j = 16 * kk + (lane & 7) + ((lane >> 4) & 1) * 8;
+      for (int kk = 0; kk < 2; ++kk) {
+        const int j = 32 * half + 16 * kk + (lane & 7) + ((lane >> 4) & 1) * 8;
         const float2 ua = *reinterpret_cast<const float2*>(&u[16 * kk + 2 * (lane & 3)]);
         const float2 ub = *reinterpret_cast<const float2*>(&u[16 * kk + 8 + 2 * (lane & 3)]);
 #pragma unroll
@@ -509,13 +509,13 @@ __device__ __forceinline__ void decay_role(const Cta& t, const LaPass& a) {
       if (active) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          uint32_t w[16];
+          uint32_t v[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            w[i] = bf16x2(x[hf][i][0], x[hf][i][1]);
-            x[hf][i][0] -= bf16_lo(w[i]), x[hf][i][1] -= bf16_hi(w[i]);
+          for (int i = 0; i < 8; ++i) {
+            v[i] = bf16x2(x[hf][i][0], x[hf][i][1]);
+            x[hf][i][0] -= bf16_lo(v[i]), x[hf][i][1] -= bf16_hi(v[i]);
           }
-          tmem_st_16x128_x8(t.tmem + ((uint32_t)(32 * q + 16 * hf) << 16) + kColUv + 32 * us, w);
+          tmem_st_16x128_x4(t.tmem + ((uint32_t)(32 * q + 16 * hf) << 16) + kColUv + 32 * us + 16 * half, v);
         }
         tmem_st_wait();
       }
@@ -549,10 +549,10 @@ __device__ __forceinline__ void put_state(uint32_t ds, const float (&S)[NC], flo
 }
 
 // Plane p of the state that step c's outputs see, to tensor memory.
-template <int NT, int PL>
+template <int NT, bool PAIR, int PL>
 __device__ __forceinline__ bool put_plane(const Cta& t, const float (&S)[NT / 2], bool active, uint32_t lanes, int half,
                                           int c, int p) {
-  constexpr int NC = NT / 2, slots = PL > 1 ? 2 : 1;
+  constexpr int NC = NT / 2, slots = PAIR ? 1 : 2;
   const int m = PL * c + p, slot = m % slots;
   if (!t.wait_free(kSpFree + slot, m / slots)) return false;
   tc_fence_after();
@@ -581,13 +581,11 @@ __device__ __forceinline__ bool put_plane(const Cta& t, const float (&S)[NT / 2]
   return true;
 }
 
-// S in registers: warp w (of 8) holds rows 32 (w % 4) .. and half of the columns; of the outputs
-// it writes the same rows and half of the block's tokens.
+// S in registers: warp w (of 8) holds rows 32 (w % 4) .. and half of the columns.
 template <int NT, bool PAIR, int PL>
 __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const Unit& un, int u, int h0) {
-  constexpr int planes = PL;
-  using L = TcSmem<NT, PAIR>;
-  constexpr int NC = NT / 2;  // columns of a thread
+  using L = TcSmem<NT, PAIR, PL>;
+  constexpr int NC = NT / 2, sp_slots = PAIR ? 1 : 2;  // columns of a thread
   const int w = threadIdx.x / 32 - kStateWarp, q = w & 3, half = w >> 2;
   const int head = PAIR ? q >> 1 : 0, h = h0 + head;
   const int r = PAIR ? (32 * q & 63) + t.lane : 32 * q + t.lane;  // value row of the head
@@ -596,7 +594,6 @@ __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const 
   const bool begins = a.reverse ? un.last : un.first, ends = a.reverse ? un.first : un.last;
   const uint32_t lanes = (uint32_t)(32 * q) << 16;
   const int64_t state_at = ((int64_t)un.seq * a.H + h) * a.NK * a.PV;
-  constexpr int sp_slots = planes > 1 ? 2 : 1;
   const uint32_t ds = t.tmem + lanes + kColDs + n0;  // the thread's part of dS
   const int count = max(0, min(NC, a.NK - n0));
   auto window_at = [&](float* base, int64_t win) { return base + ((win * a.H + h) * a.PV + r) * a.NK + n0; };
@@ -626,19 +623,92 @@ __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const 
       for (int i = 0; i < 16; ++i) S[16 * b + i] = __uint_as_float(v[i]);
     }
   }
-  // Outputs of step c: the warp's 32 rows, tokens 32 half .. 32 half + 31 of the block, 16 at a
-  // time.  Tensor memory is read in the layout of mma.sync's accumulators (registers are pairs of
-  // tokens of one row), turned by transposing stores to shared memory, and written from there
-  // in 16-byte pieces (single 2-byte stores took 16 cycles each, 5 of a block's 9 thousand).
-  uint8_t* stage = t.smem + L::kOut + w * kOutBytes;
-  uint8_t* dots_in = t.smem + L::kDot + w * kDotBytes;
-  const int row0 = r - t.lane;  // the warp's first row of the head
-  auto outputs = [&](int c) -> bool {
-    const float* rowf = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (c % kGateSlots) * L::kHeads + head)->row + 32 * half;
-    if (!t.wait(kYFull, c)) return false;
+  // windows whose state is wanted: forward, after the window's last block; reverse, before it
+  auto wanted = [&](int ci) { return a.dump && (ci == t.chunks - 1 || (ci + 1) * kC % a.window == 0); };
+  auto dump_at = [&](int ci) { return window_at(a.dump, un.first_window + ci * kC / a.window); };
+  if (a.reverse && t.chunks && wanted(t.chunks - 1)) put_state<NC>(ds, S, dump_at(t.chunks - 1), 1, count, mine);
+  tc_fence_before();
+  t.arrive(kDsFree);
+  if (!a.states_only && t.chunks)
+#pragma unroll
+    for (int p = 0; p < PL; ++p)
+      if (!put_plane<NT, PAIR, PL>(t, S, active, lanes, half, 0, p)) return;
+  for (int c = 0; c < t.chunks; ++c) {
+    const int ci = a.reverse ? t.chunks - 1 - c : c;
+    if (!t.wait(kGFull + c % kGateSlots, c / kGateSlots)) return;
+    const float dec = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (c % kGateSlots) * L::kHeads + head)->decay;
+    const bool more = !a.states_only && c + 1 < t.chunks;
+    const int m = PL * (c + 1), slot = m % sp_slots;  // the next step's first plane goes out as S is made
+    if (!t.wait(kDsFull, c) || (more && !t.wait_free(kSpFree + slot, m / sp_slots))) return;
     tc_fence_after();
-    const int64_t tok = t.token(a, c) + 32 * half;
-    const int rows = t.rows(a, c) - 32 * half;
+    const uint32_t sp = t.tmem + lanes + (slot ? kColSp1 : kColSp0) + half * (NC / 2);
+#pragma unroll
+    for (int b = 0; b < NC / 16; ++b) {
+      uint32_t d[16], v[8];
+      tmem_ld16(ds + 16 * b, d);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(S[16 * b + i], dec, __uint_as_float(d[i]));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = bf16x2(S[16 * b + 2 * i], S[16 * b + 2 * i + 1]);
+      if (more) tmem_st8(sp + 8 * b, v);
+    }
+    const int at = a.reverse ? ci - 1 : ci;  // the block whose window's state this may be
+    if (at >= 0 && wanted(at)) put_state<NC>(ds, S, dump_at(at), 1, count, mine);
+    tc_fence_before();
+    t.arrive(kDsFree);
+    t.arrive(kGFree + c % kGateSlots);
+    if (more) {
+      tmem_st_wait();
+      tc_fence_before();
+      t.arrive(kSpFull + slot);
+#pragma unroll
+      for (int p = 1; p < PL; ++p)
+        if (!put_plane<NT, PAIR, PL>(t, S, active, lanes, half, c + 1, p)) return;
+    }
+  }
+  if (a.states_only)
+    put_state<NC>(ds, S, window_at(a.carry, u), 1, count, mine);
+  else if (a.last && ends)
+    put_state<NC>(ds, S, a.last + state_at + r * a.sr + n0 * a.sc, a.sc, count, mine);
+}
+
+// Yi, Ya -> out: warp q writes rows 32 q .., 16 tokens at a time.  Tensor memory is read in the layout of mma.sync's accumulators (registers are pairs of
+// tokens of one row), turned by transposing stores to shared memory, and written from there
+// in 16-byte pieces (single 2-byte stores took 16 cycles each, 5 of a block's 9 thousand).
+template <int NT, bool PAIR, int PL>
+__device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) {
+  using L = TcSmem<NT, PAIR, PL>;
+  const int q = threadIdx.x / 32 & 3;
+  const int head = PAIR ? q >> 1 : 0, h = h0 + head;
+  const int row0 = PAIR ? 32 * q & 63 : 32 * q;  // the warp's first row of the head
+  const bool active = row0 < a.PV;
+  const uint32_t lanes = (uint32_t)(32 * q) << 16;
+  uint8_t* stage = t.smem + L::kOut + q * kOutBytes;
+  uint8_t* dots_in = t.smem + L::kDot + q * kDotBytes;
+  // The rows that step c's outputs are multiplied with, on their way while its products run.
+  auto fetch_dots = [&](int c) {
+    const int64_t tok = t.token(a, c);
+    const int rows = t.rows(a, c);
+    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.dot) + (tok * a.dot_heads + h / a.dot_div) * a.PV + row0;
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      const int i = 8 * k + (t.lane >> 2), p = (t.lane & 3) * 8;
+      const bool in = i < rows && row0 + p < a.PV;
+      const void* src = in ? from + (int64_t)i * a.dot_heads * a.PV + p : static_cast<const __nv_bfloat16*>(a.dot);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dots_in + i * kOutPitch + p * 2)),
+                   "l"(src), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+    cp_async_commit();
+  };
+  for (int c = 0; c < t.chunks; ++c) {
+    if constexpr (PL > 1) fetch_dots(c);
+    const float* rowf = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (c % kGateSlots) * L::kHeads + head)->row;
+    if (!t.wait(kGFull + c % kGateSlots, c / kGateSlots) || !t.wait(kYFull, c)) return;
+    tc_fence_after();
+    const int64_t tok = t.token(a, c);
+    const int rows = t.rows(a, c);
     const int64_t pitch = (int64_t)a.H * a.PV, at = tok * pitch + (int64_t)h * a.PV + row0;
     const int gr = t.lane >> 2, gc = (t.lane & 3) * 2;
     if constexpr (PL > 1) {
@@ -646,18 +716,18 @@ __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const 
       __syncwarp();
     }
 #pragma unroll 1
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {
       uint32_t yi[2][8], ya[2][8];
       if (active) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t from = t.tmem + lanes + ((uint32_t)(16 * hf) << 16) + 32 * half + 16 * b;
+          const uint32_t from = t.tmem + lanes + ((uint32_t)(16 * hf) << 16) + 16 * b;
           tmem_ld_16x256_x2(from + kColYi, yi[hf]);
           tmem_ld_16x256_x2(from + kColYa + (PAIR ? kC * head : 0), ya[hf]);
         }
         tmem_ld_wait();
       }
-      if (b) {
+      if (b == 3) {
         tc_fence_before();
         t.arrive(kYFree);
       }
@@ -734,73 +804,7 @@ __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const 
       }
     }
     t.arrive(kGFree + c % kGateSlots);
-    return true;
-  };
-  // The rows that step c's outputs are multiplied with, on their way while S is updated.
-  auto fetch_dots = [&](int c) {
-    const int64_t tok = t.token(a, c) + 32 * half;
-    const int rows = t.rows(a, c) - 32 * half;
-    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.dot) + (tok * a.dot_heads + h / a.dot_div) * a.PV + row0;
-#pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-      const int i = 8 * k + (t.lane >> 2), p = (t.lane & 3) * 8;
-      const bool in = i < rows && row0 + p < a.PV;
-      const void* src = in ? from + (int64_t)i * a.dot_heads * a.PV + p : static_cast<const __nv_bfloat16*>(a.dot);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dots_in + i * kOutPitch + p * 2)),
-                   "l"(src), "r"(in ? 16 : 0)
-                   : "memory");
-    }
-    cp_async_commit();
-  };
-
-  constexpr int early = planes < sp_slots ? planes : sp_slots;
-  // windows whose state is wanted: forward, after the window's last block; reverse, before it
-  auto wanted = [&](int ci) { return a.dump && (ci == t.chunks - 1 || (ci + 1) * kC % a.window == 0); };
-  auto dump_at = [&](int ci) { return window_at(a.dump, un.first_window + ci * kC / a.window); };
-  if (a.reverse && t.chunks && wanted(t.chunks - 1)) put_state<NC>(ds, S, dump_at(t.chunks - 1), 1, count, mine);
-  tc_fence_before();
-  t.arrive(kDsFree);
-  if (!a.states_only && t.chunks)
-#pragma unroll
-    for (int p = 0; p < planes; ++p)
-      if (!put_plane<NT, PL>(t, S, active, lanes, half, 0, p)) return;
-  for (int c = 0; c < t.chunks; ++c) {
-    const int ci = a.reverse ? t.chunks - 1 - c : c;
-    if constexpr (PL > 1) fetch_dots(c);
-    if (!t.wait(kGFull + c % kGateSlots, c / kGateSlots)) return;
-    const float dec = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (c % kGateSlots) * L::kHeads + head)->decay;
-    if (!t.wait(kDsFull, c)) return;
-    tc_fence_after();
-#pragma unroll
-    for (int b = 0; b < NC / 16; ++b) {
-      uint32_t d[16];
-      tmem_ld16(ds + 16 * b, d);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(S[16 * b + i], dec, __uint_as_float(d[i]));
-    }
-    const int at = a.reverse ? ci - 1 : ci;  // the block whose window's state this may be
-    if (at >= 0 && wanted(at)) put_state<NC>(ds, S, dump_at(at), 1, count, mine);
-    tc_fence_before();
-    t.arrive(kDsFree);
-    if (a.states_only) {
-      t.arrive(kGFree + c % kGateSlots);
-      continue;
-    }
-    // The next step's planes go out before this step's outputs, as far as their slots do not
-    // wait for the products behind those outputs.
-    const bool more = c + 1 < t.chunks;
-#pragma unroll
-    for (int p = 0; p < planes; ++p) {
-      if (p == early && !outputs(c)) return;
-      if (more && !put_plane<NT, PL>(t, S, active, lanes, half, c + 1, p)) return;
-    }
-    if (early == planes && !outputs(c)) return;
   }
-  if (a.states_only)
-    put_state<NC>(ds, S, window_at(a.carry, u), 1, count, mine);
-  else if (a.last && ends)
-    put_state<NC>(ds, S, a.last + state_at + r * a.sr + n0 * a.sc, a.sc, count, mine);
 }
 
 // Grid: units x heads (or pairs of heads), heads fastest.
@@ -808,7 +812,7 @@ template <int NT, bool PAIR, int PL>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     la_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ LaPass a, unsigned int* status, long long limit, int withhold) {
-  using L = TcSmem<NT, PAIR>;
+  using L = TcSmem<NT, PAIR, PL>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
   const int lanes_of_heads = PAIR ? a.H / 2 : a.H;
@@ -818,7 +822,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   if (a.states_only && (a.reverse ? un.first : un.last)) return;  // nothing follows this window
   const int warp = threadIdx.x >> 5;
   Cta t;
-  t.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  t.smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset, so that accesses stay known as shared)
   t.bars = reinterpret_cast<uint64_t*>(t.smem + L::kBar);
   t.abort_flag = reinterpret_cast<volatile int*>(t.smem + L::kFlag);
   t.limit = limit;
@@ -832,11 +836,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
       int n = 1;
-      if (i >= kReady && i < kFree) n = 4;
-      if (i == kS1Free || i == kPFull || (i >= kUvFull && i < kUvFree)) n = 4;
-      if (i == kDsFree || i == kYFree || (i >= kSpFull && i < kSpFree)) n = 8;
+      if (i == kS1Free || (i >= kPFull && i < kPFree)) n = 4;
+      if ((i >= kReady && i < kFree) || (i >= kUvFull && i < kUvFree)) n = 8;
+      if (i == kYFree) n = 4;
+      if (i == kDsFree || (i >= kSpFull && i < kSpFree)) n = 8;
       if (i >= kGFull && i < kGFree) n = L::kHeads;
-      if (i >= kGFree && i < kDrain) n = 16;
+      if (i >= kGFree && i < kDrain) n = a.states_only ? 20 : 24;
       mbar_init(&t.bars[i], n);
     }
     *t.abort_flag = 0;
@@ -850,25 +855,28 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   tc_fence_after();
   t.tmem = s_tmem;
 
-  // Registers: 640 threads start with 96 each (61440); the warpgroups' shares after the split,
-  // 128 x (40 + 72 + 104 + 2 x 128) = 60416, fit what the launch holds.
+  // Registers: 896 threads start with 72 each (64512); the warpgroups' shares after the split,
+  // 128 x (40 + 56 + 2 x 56 + 2 x 104 + 80) = 63488, fit what the launch holds.
   if (warp < kMaskWarp) {
     set_regs_dec<40>();
     if (warp == kLoadWarp)
-      load_role<NT, PAIR>(t, a, &tq, &tk, &tv, h0);
+      load_role<NT, PAIR, PL>(t, a, &tq, &tk, &tv, h0);
     else if (warp == kMmaWarp)
       mma_role<NT, PAIR, PL>(t, a, withhold);
     else if (warp - kGateWarp < L::kHeads)
-      gate_role<NT, PAIR>(t, a, h0 + warp - kGateWarp, warp - kGateWarp, u);
+      gate_role<NT, PAIR, PL>(t, a, h0 + warp - kGateWarp, warp - kGateWarp, u);
   } else if (warp < kDecayWarp) {
-    set_regs_dec<72>();
+    set_regs_dec<56>();
     mask_role<NT, PAIR, PL>(t, a);
   } else if (warp < kStateWarp) {
+    set_regs_dec<56>();
+    decay_role<NT, PAIR, PL>(t, a);
+  } else if (warp < kOutWarp) {
     set_regs_inc<104>();
-    decay_role<NT, PAIR>(t, a);
-  } else {
-    set_regs_inc<128>();
     state_role<NT, PAIR, PL>(t, a, un, u, h0);
+  } else {
+    set_regs_inc<80>();
+    if (!a.states_only) out_role<NT, PAIR, PL>(t, a, h0);
   }
 
   __syncwarp();
@@ -897,7 +905,7 @@ bool make_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t toke
 template <int NT, bool PAIR, int PL>
 cudaError_t launch_one(const LaPass& p, cudaStream_t st) {
   auto* fn = la_tc_kernel<NT, PAIR, PL>;
-  using L = TcSmem<NT, PAIR>;
+  using L = TcSmem<NT, PAIR, PL>;
   static_assert(L::kBytes <= 227 * 1024, "tiles must fit the SM's shared memory");
   CUtensorMap tq, tk, tv;
   if (!make_map(&tq, p.query, p.NK, p.q_heads, p.tokens) || !make_map(&tk, p.key, p.NK, p.k_heads, p.tokens) ||
