@@ -79,9 +79,9 @@ struct Gate {
   float decay, pad[3];
 };
 
-// An output warp's own staging: 16 tokens x 32 rows of outputs (bf16: 80 bytes a token, fp32: 144;
-// neither pitch has bank conflicts), and 64 tokens x 32 rows of bf16.
-constexpr int kOutBytes = 16 * 144, kOutPitch = 80, kOutPitch32 = 144, kDotBytes = kC * kOutPitch;
+// An output warp's own staging: 64 tokens x 32 rows of bf16 at 80 bytes a token, or 16 tokens of
+// fp32 at 144 (neither pitch has bank conflicts); and as much for the rows of the dot products.
+constexpr int kOutPitch = 80, kOutPitch32 = 144, kOutBytes = kC * kOutPitch, kDotBytes = kC * kOutPitch;
 
 template <int NT, bool PAIR, int PL>
 struct TcSmem {
@@ -715,6 +715,8 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
       cp_async_wait_all();
       __syncwarp();
     }
+    // Everything is read, and Yi and Ya are free for the next block's products, before anything
+    // goes to memory: the products and this reading alternate, and are most of a block's time.
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
       uint32_t yi[2][8], ya[2][8];
@@ -731,7 +733,6 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
         tc_fence_before();
         t.arrive(kYFree);
       }
-      if (!active) continue;
       const float2 f0 = *reinterpret_cast<const float2*>(&rowf[16 * b + gc]);
       const float2 f1 = *reinterpret_cast<const float2*>(&rowf[16 * b + 8 + gc]);
       float o[2][8];  // [half of the rows][4 tile of 8 tokens + 2 (row + 8) + token of the pair]
@@ -741,7 +742,16 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
         for (int e = 0; e < 8; ++e)
           o[hf][e] = fmaf(__uint_as_float(yi[hf][e]), e < 4 ? (e & 1 ? f0.y : f0.x) : (e & 1 ? f1.y : f1.x),
                           __uint_as_float(ya[hf][e]));
-      if (a.out_f32) {
+      if (!a.out_f32) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint8_t* to = stage + (16 * b + 8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf + 16 * ((t.lane >> 3) & 1);
+          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(to)),
+                       "r"(bf16x2(o[hf][0], o[hf][1])), "r"(bf16x2(o[hf][2], o[hf][3])),
+                       "r"(bf16x2(o[hf][4], o[hf][5])), "r"(bf16x2(o[hf][6], o[hf][7]))
+                       : "memory");
+        }
+      } else if (active) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
@@ -756,26 +766,10 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
           const float4 v = *reinterpret_cast<const float4*>(stage + i * kOutPitch32 + p * 4);
           if (16 * b + i < rows && row0 + p < a.PV) *reinterpret_cast<float4*>(to + i * pitch + p) = v;
         }
-      } else {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint8_t* to = stage + (8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf + 16 * ((t.lane >> 3) & 1);
-          asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(to)),
-                       "r"(bf16x2(o[hf][0], o[hf][1])), "r"(bf16x2(o[hf][2], o[hf][3])),
-                       "r"(bf16x2(o[hf][4], o[hf][5])), "r"(bf16x2(o[hf][6], o[hf][7]))
-                       : "memory");
-        }
         __syncwarp();
-        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at + 16 * b * pitch;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int i = 8 * k + gr, p = (t.lane & 3) * 8;
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + i * kOutPitch + p * 2);
-          if (16 * b + i < rows && row0 + p < a.PV) *reinterpret_cast<uint4*>(to + i * pitch + p) = v;
-        }
       }
-      __syncwarp();
-      if constexpr (PL > 1) {  // sums over the warp's rows of out * dot, for the decay's gradient
+      if constexpr (PL > 1)
+        if (active) {  // sums over the warp's rows of out * dot, for the decay's gradient
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -804,6 +798,16 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
       }
     }
     t.arrive(kGFree + c % kGateSlots);
+    if (!active || a.out_f32) continue;
+    __syncwarp();
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at;
+#pragma unroll 4
+    for (int k = 0; k < 8; ++k) {
+      const int i = 8 * k + gr, p = (t.lane & 3) * 8;
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + i * kOutPitch + p * 2);
+      if (i < rows && row0 + p < a.PV) *reinterpret_cast<uint4*>(to + i * pitch + p) = v;
+    }
+    __syncwarp();
   }
 }
 
@@ -856,7 +860,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   t.tmem = s_tmem;
 
   // Registers: 896 threads start with 72 each (64512); the warpgroups' shares after the split,
-  // 128 x (40 + 56 + 2 x 56 + 2 x 104 + 80) = 63488, fit what the launch holds.
+  // 128 x (40 + 56 + 2 x 56 + 2 x 112 + 72) = 64512, are what the launch holds.
   if (warp < kMaskWarp) {
     set_regs_dec<40>();
     if (warp == kLoadWarp)
@@ -872,10 +876,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     set_regs_dec<56>();
     decay_role<NT, PAIR, PL>(t, a);
   } else if (warp < kOutWarp) {
-    set_regs_inc<104>();
+    set_regs_inc<112>();
     state_role<NT, PAIR, PL>(t, a, un, u, h0);
   } else {
-    set_regs_inc<80>();
+    set_regs_inc<72>();
     if (!a.states_only) out_role<NT, PAIR, PL>(t, a, h0);
   }
 
