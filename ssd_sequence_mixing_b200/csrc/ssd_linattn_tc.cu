@@ -17,9 +17,11 @@
 // One CTA per SM takes one head (up to 128 value rows), or two heads of up to 64 rows each
 // that share query and key, and walks the blocks of its unit.  28 warps, each with one task, so
 // that the tasks of several blocks overlap without any of them being interleaved by hand:
-//   load  (1 warp)   query, key, value tiles by TMA, three stages
-//   mma   (1 warp)   issues every product
-//   gates (2 warps)  a head each: the sums of log-decays in 64 bits and the factors from them
+//   load  (1 warp)   query, key, value tiles by TMA, three stages; issues S1
+//   dS    (1 warp)   issues the products of dS
+//   Y     (1 warp)   issues Yi and Ya (one warp for all products took 110 cycles for each of a
+//                    block's 32 and 10 commits, and was what a block's time was made of)
+//   gates (1 warp)   the sums of log-decays in 64 bits and the factors from them
 //   mask  (4 warps)  S1 -> P
 //   decay (8 warps)  value -> the planes of upd o value, by transposing loads
 //   state (8 warps)  dS -> S -> the bf16 planes of S
@@ -37,6 +39,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "sm100_ptx.cuh"
 #include "ssd.h"
 #include "ssd_common.cuh"
@@ -53,11 +57,12 @@ constexpr int kC = kLaChunk;  // tokens of a block
 constexpr int kAtomBytes = kC * 128;  // 64 tokens x 64 columns of bf16, 128-byte rows
 constexpr int kMaxStages = 3, kGateSlots = 4, kPlanes = 3;
 constexpr int kWarpsTc = 28, kThreadsTc = 32 * kWarpsTc;
-constexpr int kLoadWarp = 0, kMmaWarp = 1, kGateWarp = 2, kMaskWarp = 4, kDecayWarp = 8, kStateWarp = 16, kOutWarp = 24;
+constexpr int kLoadWarp = 0, kDsWarp = 1, kGateWarp = 2, kYWarp = 3, kMaskWarp = 4, kDecayWarp = 8, kStateWarp = 16, kOutWarp = 24;
 
 // tensor memory columns
 constexpr int kColS1 = 0, kColYi = 64, kColYa = 128, kColDs = 256, kColUv = 384, kColSp0 = 448, kColSp1 = 192;
 constexpr int kTmem = 512;
+constexpr uint32_t kDrainPolls = 1u << 22;  // (a drain's bound is not the test hooks' to lower)
 
 enum Bar {
   kFull = 0,                     // tiles of a stage have landed
@@ -70,8 +75,8 @@ enum Bar {
   kSpFull, kSpFree = kSpFull + 2,
   kYFull = kSpFree + 2, kYFree,
   kGFull, kGFree = kGFull + kGateSlots,
-  kDrain = kGFree + kGateSlots,
-  kBars
+  kDrain = kGFree + kGateSlots,  // every product of a warp that issues them is done
+  kBars = kDrain + 3
 };
 
 struct Gate {
@@ -153,16 +158,35 @@ __device__ __forceinline__ void set_regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag, long long limit) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*abort_flag) return false;
-    if (clock64() - t0 > limit) {
-      *abort_flag = 1;
-      return false;
-    }
-  }
-  return true;
+// Waits for the phase with the given parity, for at most `polls` polls of up to 1 us each (the
+// hint; a poll may also return at once).  A tight loop: the waits are a good part of the code, and
+// the block loop of all roles together has to stay in the instruction cache.
+__device__ __forceinline__ bool wait_polls(uint32_t bar, uint32_t parity, uint32_t polls) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %3;\n\t"
+      "POLL_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra POLL_%=;\n\t"
+      "DONE_%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(polls)
+      : "memory");
+  return ok != 0;
+}
+
+// 2^c of a sum of log-decays c <= 0 (up to rounding), split as c = hi + lo with hi whole: 2^lo to
+// the accuracy of ex2, times an exact power (0 below 2^-126, infinity from 2^128).  A NaN stays one.
+__device__ __forceinline__ float exp2_split(double c, float& hi, float& lo) {
+  const int whole = min(max(__double2int_rd(c), -100000), 128);
+  hi = (float)whole;
+  lo = (float)(c - (double)whole);
+  return ex2(lo) * (whole < -126 ? 0.f : __int_as_float((whole + 127) << 23));
 }
 
 // What every role needs.
@@ -170,15 +194,18 @@ struct Cta {
   uint8_t* smem;
   uint64_t* bars;
   volatile int* abort_flag;
-  long long limit;
+  uint32_t polls;
   uint32_t tmem;
   int chunks;
   int64_t t0;
   int len, lane;
-  // A whole warp waits for the n-th completion of a barrier (n from 0).
+  // A whole warp waits for the n-th completion of a barrier (n from 0).  A wait that gives up
+  // ends the role; the others' waits run out in turn.
   __device__ __forceinline__ bool wait(int bar, int n) const {
-    const bool mine = mbar_try_wait(&bars[bar], (uint32_t)n & 1u) || wait_spin(&bars[bar], (uint32_t)n & 1u, abort_flag, limit);
-    return !__any_sync(0xffffffffu, !mine);
+    const bool mine = wait_polls(smem_u32(&bars[bar]), (uint32_t)n & 1u, polls);
+    if (!__any_sync(0xffffffffu, !mine)) return true;
+    *abort_flag = 1;
+    return false;
   }
   // A producer's wait for the slot's consumers; use number n (from 0) of the slot.
   __device__ __forceinline__ bool wait_free(int bar, int n) const { return n == 0 || wait(bar, n - 1); }
@@ -196,185 +223,225 @@ struct Cta {
   }
 };
 
-template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void load_role(const Cta& t, const LaPass& a, const CUtensorMap* tq, const CUtensorMap* tk,
-                          const CUtensorMap* tv, int h0) {
-  using L = TcSmem<NT, PAIR, PL>;
-  const int qh = h0 / a.q_div, kh = h0 / a.k_div;
-  const int v_atoms = PAIR || a.PV > 64 ? 2 : 1;
-  const uint32_t bytes = ((a.states_only ? 1 : 2) * (NT / 64) + v_atoms) * kAtomBytes;
-  int c = 0;
-  for (; c < t.chunks; ++c) {
-    const int s = c % L::kStages;
-    if (!t.wait_free(kFree + s, c / L::kStages)) break;
-    if (t.lane == 0) {
-      uint64_t* bar = &t.bars[kFull + s];
-      uint8_t* base = t.smem + s * L::kStage;
-      const int tok = (int)t.token(a, c);
-      mbar_expect_tx(bar, bytes);
-#pragma unroll
-      for (int i = 0; i < NT / 64; ++i) tma_load_3d(base + L::kK + i * kAtomBytes, tk, 64 * i, kh, tok, bar);
-      for (int i = 0; i < v_atoms; ++i)
-        tma_load_3d(base + L::kV + i * kAtomBytes, tv, PAIR ? 0 : 64 * i, (PAIR ? h0 + i : h0) / a.v_div, tok, bar);
-      if (!a.states_only) {
-#pragma unroll
-        for (int i = 0; i < NT / 64; ++i) tma_load_3d(base + L::kQ + i * kAtomBytes, tq, 64 * i, qh, tok, bar);
-      }
-    }
-    __syncwarp();
-  }
-  // after a failure: what was issued lands before the CTA ends
-  if (c < t.chunks)
-    for (int d = max(0, c - L::kStages); d < c; ++d)
-      mbar_wait_bounded(&t.bars[kFull + d % L::kStages], (uint32_t)(d / L::kStages) & 1u, 1ll << 32);
-}
-
-template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void mma_role(const Cta& t, const LaPass& a, int withhold) {
-  constexpr int planes = PL;
-  using L = TcSmem<NT, PAIR, PL>;
-  const bool leader = elect_one();
-  const uint32_t base = smem_u32(t.smem);
-  const uint64_t k_major = sdesc_sw128(0, 16, 1024), mn_major = sdesc_sw128(0, kAtomBytes, 1024);
-  auto at = [&](uint64_t major, int off) { return major | (uint64_t)((base + off) >> 4); };
-  const uint32_t id_s1 = idesc_bf16(64, kC, 0, 0), id_yi = idesc_bf16(128, kC, 0, 0),
-                 id_ya = idesc_bf16(128, PAIR ? 2 * kC : kC, 1, 0), id_ds = idesc_bf16(128, NT, 0, 1);
-  constexpr int sp_slots = PAIR ? 1 : 2;
-  auto commit = [&](int bar) {
+// What the three warps that issue products share.
+struct Issue {
+  const Cta& t;
+  bool leader;
+  uint64_t k_major, mn_major;  // descriptors of shared-memory tiles, without the address
+  uint32_t base;
+  __device__ __forceinline__ explicit Issue(const Cta& cta)
+      : t(cta), leader(elect_one()), k_major(sdesc_sw128(0, 16, 1024)), mn_major(sdesc_sw128(0, kAtomBytes, 1024)),
+        base(smem_u32(cta.smem)) {}
+  __device__ __forceinline__ uint64_t at(uint64_t major, int off) const { return major | (uint64_t)((base + off) >> 4); }
+  // K step kk of a K-major tile of 64-column atoms
+  static __device__ __forceinline__ uint64_t koff(int kk) { return (uint64_t)(((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4); }
+  // Arrives on the barrier once every product this warp has issued so far is done.
+  __device__ __forceinline__ void commit(int bar) const {
     if (leader) umma_commit(&t.bars[bar]);
     __syncwarp();
-  };
-  auto koff = [](int kk) { return (uint64_t)(((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4); };
-  auto s1 = [&](int c) -> bool {
-    const int s = c % L::kStages;
-    // the tiles as they landed: what a last block holds past its end is masked in P
-    if (!t.wait(kFull + s, c / L::kStages) || !t.wait_free(kS1Free, c)) return false;
-    tc_fence_after();
-    if (leader) {
-      const uint64_t q = at(k_major, s * L::kStage + L::kQ), k = at(k_major, s * L::kStage + L::kK);
+  }
+  __device__ __forceinline__ void drain(int bar) const {
+    commit(bar);
+    if (!wait_polls(smem_u32(&t.bars[bar]), 0, kDrainPolls)) *t.abort_flag = 1;
+  }
+};
+
+// Tiles by TMA, and S1 of each block.
+template <int NT, bool PAIR, int PL>
+__device__ __forceinline__ void load_role(const Cta& t, const LaPass& a, const CUtensorMap* tq, const CUtensorMap* tk,
+                                          const CUtensorMap* tv, int h0, int withhold) {
+  using L = TcSmem<NT, PAIR, PL>;
+  const Issue mma(t);
+  const int qh = h0 / a.q_div, kh = h0 / a.k_div, vh = h0 / a.v_div;  // (two heads: v_div is 1)
+  const int v_atoms = PAIR || a.PV > 64 ? 2 : 1;
+  const uint32_t bytes = ((a.states_only ? 1 : 2) * (NT / 64) + v_atoms) * kAtomBytes;
+  constexpr uint32_t id_s1 = idesc_bf16(64, kC, 0, 0);
+  constexpr int kAhead = L::kStages - 1;  // blocks loaded before they are needed
+  bool ok = true;
+  int s = 0, use = 0, ls = 0, luse = 0;  // stage and its use: of the products, of the loads
 #pragma unroll 1
-      for (int kk = 0; kk < NT / 16; ++kk) umma_f16(t.tmem + kColS1, q + koff(kk), k + koff(kk), id_s1, kk > 0);
+  for (int c = -kAhead; c < t.chunks; ++c) {
+    if (c >= 0 && !a.states_only) {
+      // the tiles as they landed: what a last block holds past its end is masked in P
+      if (!(ok = t.wait(kFull + s, use)) || !(ok = t.wait_free(kS1Free, c))) break;
+      tc_fence_after();
+      if (mma.leader) {
+        const uint64_t q = mma.at(mma.k_major, s * L::kStage + L::kQ), k = mma.at(mma.k_major, s * L::kStage + L::kK);
+#pragma unroll
+        for (int kk = 0; kk < NT / 16; ++kk)
+          umma_f16(t.tmem + kColS1, q + Issue::koff(kk), k + Issue::koff(kk), id_s1, kk > 0);
+      }
+      __syncwarp();
+      if (!withhold) mma.commit(kS1Full);
+      if (++s == L::kStages) s = 0, ++use;
+    }
+    if (c + kAhead >= t.chunks) continue;
+    if (!(ok = t.wait_free(kFree + ls, luse))) break;
+    if (t.lane == 0) {
+      uint64_t* bar = &t.bars[kFull + ls];
+      uint8_t* to = t.smem + ls * L::kStage;
+      const int tok = (int)t.token(a, c + kAhead);
+      mbar_expect_tx(bar, bytes);
+#pragma unroll
+      for (int i = 0; i < NT / 64; ++i) tma_load_3d(to + L::kK + i * kAtomBytes, tk, 64 * i, kh, tok, bar);
+      if (!a.states_only) {
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) tma_load_3d(to + L::kQ + i * kAtomBytes, tq, 64 * i, qh, tok, bar);
+      }
+      tma_load_3d(to + L::kV, tv, 0, vh, tok, bar);
+      if (v_atoms == 2) tma_load_3d(to + L::kV + kAtomBytes, tv, PAIR ? 0 : 64, PAIR ? vh + 1 : vh, tok, bar);
     }
     __syncwarp();
-    if (!withhold) commit(kS1Full);
-    return true;
-  };
-  bool ok = true;
-  if (!a.states_only && t.chunks) ok = s1(0);
-  for (int c = 0; ok && c < t.chunks; ++c) {
-    const int s = c % L::kStages;
-    if (!a.states_only) {
-      if (c + 1 < t.chunks && !(ok = s1(c + 1))) break;
+    if (++ls == L::kStages) ls = 0, ++luse;
+  }
+  mma.drain(kDrain);
+  // after a failure: what was issued lands before the CTA ends
+  if (!ok)
+#pragma unroll 1
+    for (int d = 0; d < L::kStages; ++d) {
+      const int n = luse - (d >= ls);  // the last use of stage d that was loaded
+      if (n >= 0) wait_polls(smem_u32(&t.bars[kFull + d]), (uint32_t)n & 1u, kDrainPolls);
     }
-    // dS = (upd o value)^T key, plane by plane
-    if (!(ok = t.wait(kReady + s, c / L::kStages)) || !(ok = t.wait(kDsFree, c))) break;  // (the first time: S is loaded)
-    const uint64_t k_mn = at(mn_major, s * L::kStage + L::kK);
+}
+
+// dS = (upd o value)^T key, plane by plane.
+template <int NT, bool PAIR, int PL>
+__device__ __forceinline__ void ds_role(const Cta& t, const LaPass& a) {
+  using L = TcSmem<NT, PAIR, PL>;
+  const Issue mma(t);
+  constexpr uint32_t id_ds = idesc_bf16(128, NT, 0, 1);
+  bool ok = true;
+  int s = 0, use = 0;
+#pragma unroll 1
+  for (int c = 0; ok && c < t.chunks; ++c) {
+    if (!(ok = t.wait(kReady + s, use)) || !(ok = t.wait(kDsFree, c))) break;  // (the first time: S is loaded)
+    const uint64_t k_mn = mma.at(mma.mn_major, s * L::kStage + L::kK);
 #pragma unroll 1
     for (int p = 0; p < kPlanes; ++p) {
       const int m = kPlanes * c + p, slot = m & 1;
       if (!(ok = t.wait(kUvFull + slot, m >> 1))) break;
       tc_fence_after();
-      if (leader) {
-#pragma unroll 1
+      if (mma.leader) {
+#pragma unroll
         for (int kk = 0; kk < kC / 16; ++kk)
           umma_f16_ta(t.tmem + kColDs, t.tmem + kColUv + slot * 32 + kk * 8, k_mn + kk * 128, id_ds, p > 0 || kk > 0);
       }
       __syncwarp();
-      commit(kUvFree + slot);
+      mma.commit(kUvFree + slot);
     }
     if (!ok) break;
-    commit(kDsFull);
-    if (a.states_only) {
-      commit(kFree + s);
-      continue;
-    }
-    // Yi^T = S query^T
-    if (!(ok = t.wait_free(kYFree, c))) break;
-    const uint64_t q = at(k_major, s * L::kStage + L::kQ);
+    mma.commit(kDsFull);
+    mma.commit(kFree + s);
+    if (++s == L::kStages) s = 0, ++use;
+  }
+  mma.drain(kDrain + 1);
+}
+
+// Yi^T = S query^T and Ya^T = value^T P^T.
+template <int NT, bool PAIR, int PL>
+__device__ __forceinline__ void y_role(const Cta& t, const LaPass& a) {
+  using L = TcSmem<NT, PAIR, PL>;
+  const Issue mma(t);
+  constexpr uint32_t id_yi = idesc_bf16(128, kC, 0, 0), id_ya = idesc_bf16(128, PAIR ? 2 * kC : kC, 1, 0);
+  constexpr int sp_slots = PAIR ? 1 : 2;
+  bool ok = true;
+  int s = 0, use = 0;
 #pragma unroll 1
-    for (int p = 0; p < planes; ++p) {
-      const int m = planes * c + p, slot = m % sp_slots;
+  for (int c = 0; ok && c < t.chunks; ++c) {
+    if (!(ok = t.wait(kFull + s, use)) || !(ok = t.wait_free(kYFree, c))) break;
+    const uint64_t q = mma.at(mma.k_major, s * L::kStage + L::kQ);
+#pragma unroll 1
+    for (int p = 0; p < PL; ++p) {
+      const int m = PL * c + p, slot = m % sp_slots;
       if (!(ok = t.wait(kSpFull + slot, m / sp_slots))) break;
       tc_fence_after();
-      if (leader) {
+      if (mma.leader) {
         const uint32_t sp = t.tmem + (slot ? kColSp1 : kColSp0);
-#pragma unroll 1
+#pragma unroll
         for (int kk = 0; kk < NT / 16; ++kk)
-          umma_f16_ta(t.tmem + kColYi, sp + kk * 8, q + koff(kk), id_yi, p > 0 || kk > 0);
+          umma_f16_ta(t.tmem + kColYi, sp + kk * 8, q + Issue::koff(kk), id_yi, p > 0 || kk > 0);
       }
       __syncwarp();
-      commit(kSpFree + slot);
+      mma.commit(kSpFree + slot);
     }
     if (!ok) break;
-    // Ya^T = value^T P^T
-    if (!(ok = t.wait(kPFull + (c & 1), c >> 1))) break;
+    if (!(ok = t.wait(kReady + s, use)) || !(ok = t.wait(kPFull + (c & 1), c >> 1))) break;
     tc_fence_after();
-    if (leader) {
-      const uint64_t v_mn = at(mn_major, s * L::kStage + L::kV);
-      for (int p = 0; p < planes; ++p) {
-        const uint64_t pm = at(k_major, L::kP + ((c & 1) * L::kPTiles + p) * kAtomBytes);
+    if (mma.leader) {
+      const uint64_t v_mn = mma.at(mma.mn_major, s * L::kStage + L::kV);
 #pragma unroll 1
+      for (int p = 0; p < PL; ++p) {
+        const uint64_t pm = mma.at(mma.k_major, L::kP + ((c & 1) * L::kPTiles + p) * kAtomBytes);
+#pragma unroll
         for (int kk = 0; kk < kC / 16; ++kk)
           umma_f16(t.tmem + kColYa, v_mn + kk * 128, pm + kk * 2, id_ya, p > 0 || kk > 0);
       }
     }
     __syncwarp();
-    commit(kPFree + (c & 1));
-    commit(kYFull);
-    commit(kFree + s);
+    mma.commit(kPFree + (c & 1));
+    mma.commit(kYFull);
+    mma.commit(kFree + s);  // (S1 of this block was done before its P)
+    if (++s == L::kStages) s = 0, ++use;
   }
-  commit(kDrain);
-  if (!mbar_wait_bounded(&t.bars[kDrain], 0, 1ll << 32)) *t.abort_flag = 1;
+  mma.drain(kDrain + 2);
 }
 
-// One warp per head: lane l takes tokens 2 l and 2 l + 1 of each block.
+// One head: lane l takes tokens 2 l, 2 l + 1 of each block.  Two: half a warp each, 4 tokens a lane.
 template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void gate_role(const Cta& t, const LaPass& a, int h, int which, int unit) {
+__device__ __forceinline__ void gate_role(const Cta& t, const LaPass& a, int h0, int unit) {
   using L = TcSmem<NT, PAIR, PL>;
-  const int i0 = 2 * t.lane;
+  constexpr int kLanes = 32 / L::kHeads, kTok = kC / kLanes;
+  const int which = PAIR ? t.lane >> 4 : 0, l = t.lane & (kLanes - 1), i0 = kTok * l, h = h0 + which;
   const float sr = a.reverse ? 1.f : a.scale, su = a.reverse ? a.scale : 1.f;
+  const float* from = a.log_decay + h;
   double total = 0.0;
-  auto load = [&](int c, float& x, float& y) {
-    x = y = 0.f;
+  float x[kTok];
+  auto load = [&](int c) {
     if (c >= t.chunks) return;
     const int64_t tok = t.token(a, c) + i0;
-    const int rows = t.rows(a, c);
-    if (i0 < rows) x = a.log_decay[a.per_token ? tok * a.H + h : h];
-    if (i0 + 1 < rows) y = a.log_decay[a.per_token ? (tok + 1) * a.H + h : h];
-  };
-  float x, y;
-  load(0, x, y);
-  for (int c = 0; c < t.chunks; ++c) {
-    const double l0 = log2_clamped(x), l1 = log2_clamped(y);
-    load(c + 1, x, y);
-    double c1 = l0 + l1;
+    const int left = t.rows(a, c) - i0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, c1, o);
-      if (t.lane >= o) c1 += v;
+    for (int j = 0; j < kTok; ++j) x[j] = j < left ? from[a.per_token ? (tok + j) * a.H : 0] : 0.f;
+  };
+  load(0);
+#pragma unroll 1
+  for (int c = 0; c < t.chunks; ++c) {
+    double sum[kTok];  // inclusive sums from the block's start
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) sum[j] = log2_clamped(x[j]) + (j ? sum[j - 1] : 0.0);
+    load(c + 1);
+    double before = sum[kTok - 1];
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) {
+      const double v = __shfl_up_sync(0xffffffffu, before, o, kLanes);
+      if (l >= o) before += v;
     }
-    const double end = __shfl_sync(0xffffffffu, c1, 31), c0 = c1 - l1;
+    const double end = __shfl_sync(0xffffffffu, before, kLanes - 1, kLanes);
+    before -= sum[kTok - 1];
     const int slot = c % kGateSlots;
     if (!t.wait_free(kGFree + slot, c / kGateSlots)) return;
     Gate* g = reinterpret_cast<Gate*>(t.smem + L::kGate) + slot * L::kHeads + which;
-    float hi[2], lo[2], row[2], upd[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const double cc = j ? c1 : c0, f = floor(cc), e = floor(end - cc);
-      hi[j] = (float)f, lo[j] = (float)(cc - f);
-      const float from_start = exp2_parts(hi[j], lo[j]), to_end = exp2_parts((float)e, (float)(end - cc - e));
-      row[j] = (a.reverse ? to_end : from_start) * sr;
-      upd[j] = (a.reverse ? from_start : to_end) * su;
+    for (int j = 0; j < kTok; ++j) {
+      const double cc = before + sum[j];
+      float hi, lo;
+      const float from_start = exp2_split(cc, hi, lo);
+      g->chi[i0 + j] = hi, g->clo[i0 + j] = lo;
+      const float to_end = exp2_split(end - cc, hi, lo);
+      g->row[i0 + j] = (a.reverse ? to_end : from_start) * sr;
+      g->upd[i0 + j] = (a.reverse ? from_start : to_end) * su;
     }
-    *reinterpret_cast<float2*>(&g->chi[i0]) = make_float2(hi[0], hi[1]);
-    *reinterpret_cast<float2*>(&g->clo[i0]) = make_float2(lo[0], lo[1]);
-    *reinterpret_cast<float2*>(&g->row[i0]) = make_float2(row[0], row[1]);
-    *reinterpret_cast<float2*>(&g->upd[i0]) = make_float2(upd[0], upd[1]);
-    if (t.lane == 0) g->decay = exp2f((float)end);
+    if (l == 0) {
+      float hi, lo;
+      g->decay = exp2_split(end, hi, lo);
+    }
     total += end;
     t.arrive(kGFull + slot);
   }
-  if (a.states_only && t.lane == 0) a.window_decay[(int64_t)unit * a.H + h] = exp2_parts((float)floor(total), (float)(total - floor(total)));
+  if (a.states_only && l == 0) {
+    float hi, lo;
+    a.window_decay[(int64_t)unit * a.H + h] = exp2_split(total, hi, lo);
+  }
 }
 
 // S1 -> P.  Warp q holds rows 16 q .. 16 q + 15 of S1 (lanes 0 .. 15 of its quarter of tensor
@@ -401,6 +468,7 @@ __device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
         put(P + p * kAtomBytes, i0 + 8, 8 * n + gc, 0u);
       }
   }
+#pragma unroll 1
   for (int c = 0; c < t.chunks; ++c) {
     const int slot = c % kGateSlots;
     if (!t.wait(kGFull + slot, c / kGateSlots)) return;
@@ -408,22 +476,19 @@ __device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
       const Gate* g = reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads;
       if (!t.wait(kS1Full, c) || !t.wait_free(kPFree + (c & 1), c >> 1)) return;
       tc_fence_after();
+      // the column tiles with any j in reach, two at a time
+      const int b0 = a.reverse ? q : 0, b1 = a.reverse ? 4 : q + 1;
 #pragma unroll 1
-      for (int b = 0; b < 2; ++b) {  // 32 columns at a time
-        uint32_t r[16];
-        tmem_ld_16x256_x4(t.tmem + ((uint32_t)(32 * q) << 16) + kColS1 + 32 * b, r);
+      for (int b = b0; b < b1; ++b) {
+        uint32_t r[8];
+        tmem_ld_16x256_x2(t.tmem + ((uint32_t)(32 * q) << 16) + kColS1 + 16 * b, r);
         tmem_ld_wait();
-        if (b) {
-          tc_fence_before();
-          t.arrive(kS1Free);
-        }
 #pragma unroll
         for (int hh = 0; hh < L::kHeads; ++hh) {
           const float hi0 = g[hh].chi[i0], hi1 = g[hh].chi[i0 + 8], lo0 = g[hh].clo[i0], lo1 = g[hh].clo[i0 + 8];
 #pragma unroll
-          for (int nn = 0; nn < 4; ++nn) {
-            const int n = 4 * b + nn, j = 8 * n + gc;
-            if (a.reverse ? n < 2 * q : n > 2 * q + 1) continue;
+          for (int nn = 0; nn < 2; ++nn) {
+            const int j = 16 * b + 8 * nn + gc;
             const float2 hj = *reinterpret_cast<const float2*>(&g[hh].chi[j]);
             const float2 lj = *reinterpret_cast<const float2*>(&g[hh].clo[j]);
             float v[4];
@@ -445,6 +510,8 @@ __device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
           }
         }
       }
+      tc_fence_before();
+      t.arrive(kS1Free);
       fence_proxy_async();
       t.arrive(kPFull + (c & 1));
     }
@@ -460,21 +527,25 @@ __device__ __forceinline__ void decay_role(const Cta& t, const LaPass& a) {
   const int w = threadIdx.x / 32 - kDecayWarp, q = w & 3, half = w >> 2, lane = t.lane;
   const int head = PAIR ? q >> 1 : 0;
   const bool active = (PAIR ? 32 * q & 63 : 32 * q) < a.PV;
+  int s = 0, use = 0;
+#pragma unroll 1
   for (int c = 0; c < t.chunks; ++c) {
-    const int s = c % L::kStages, slot = c % kGateSlots, rows = t.rows(a, c);
+    const int slot = c % kGateSlots, rows = t.rows(a, c);
     uint8_t* tiles = t.smem + s * L::kStage;
-    if (!t.wait(kFull + s, c / L::kStages)) return;
+    if (!t.wait(kFull + s, use)) return;
     if (rows < kC) {
-      // the sequence ends inside the block: what follows is another's, and 0 * NaN is NaN
-      const int atoms = L::kStage / kAtomBytes - NT / 64;  // key and value
-      for (int e = threadIdx.x & 255; e < (kC - rows) * 8 * atoms; e += 256) {
-        const int at = e / ((kC - rows) * 8), x = e % ((kC - rows) * 8);
-        *reinterpret_cast<uint4*>(tiles + L::kK + at * kAtomBytes + (rows + x / 8) * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
-      }
+      // the sequence ends inside the block: what follows is another's, and 0 * NaN is NaN.  A
+      // row of key and value is 8 pieces of 16 bytes in each of up to 4 atoms
+      constexpr int kAtoms = NT / 64 + 2;
+#pragma unroll 1
+      for (int i = rows + w; i < kC; i += 8)
+        if (lane < 8 * kAtoms)
+          *reinterpret_cast<uint4*>(tiles + L::kK + (lane >> 3) * kAtomBytes + i * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
       fence_proxy_async();
     }
     t.arrive(kReady + s);
-    if (rows < kC && !t.wait(kReady + s, c / L::kStages)) return;
+    if (rows < kC && !t.wait(kReady + s, use)) return;
+    if (++s == L::kStages) s = 0, ++use;
     if (!t.wait(kGFull + slot, c / kGateSlots)) return;
     const float* u = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads + head)->upd + 32 * half;
     float x[2][8][2];  // [half of the rows][4 k step of 16 tokens + matrix][token of the pair]
@@ -633,6 +704,7 @@ __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const 
 #pragma unroll
     for (int p = 0; p < PL; ++p)
       if (!put_plane<NT, PAIR, PL>(t, S, active, lanes, half, 0, p)) return;
+#pragma unroll 1
   for (int c = 0; c < t.chunks; ++c) {
     const int ci = a.reverse ? t.chunks - 1 - c : c;
     if (!t.wait(kGFull + c % kGateSlots, c / kGateSlots)) return;
@@ -702,6 +774,7 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
     }
     cp_async_commit();
   };
+#pragma unroll 1
   for (int c = 0; c < t.chunks; ++c) {
     if constexpr (PL > 1) fetch_dots(c);
     const float* rowf = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (c % kGateSlots) * L::kHeads + head)->row;
@@ -815,7 +888,7 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
 template <int NT, bool PAIR, int PL>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     la_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ LaPass a, unsigned int* status, long long limit, int withhold) {
+                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ LaPass a, unsigned int* status, uint32_t polls, int withhold) {
   using L = TcSmem<NT, PAIR, PL>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
@@ -829,7 +902,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   t.smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset, so that accesses stay known as shared)
   t.bars = reinterpret_cast<uint64_t*>(t.smem + L::kBar);
   t.abort_flag = reinterpret_cast<volatile int*>(t.smem + L::kFlag);
-  t.limit = limit;
+  t.polls = polls;
   t.lane = threadIdx.x & 31;
   t.t0 = un.t0, t.len = un.len;
   t.chunks = (un.len + kC - 1) / kC;
@@ -844,7 +917,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if ((i >= kReady && i < kFree) || (i >= kUvFull && i < kUvFree)) n = 8;
       if (i == kYFree) n = 4;
       if (i == kDsFree || (i >= kSpFull && i < kSpFree)) n = 8;
-      if (i >= kGFull && i < kGFree) n = L::kHeads;
+      if (i >= kFree && i < kS1Full) n = a.states_only ? 1 : 2;
       if (i >= kGFree && i < kDrain) n = a.states_only ? 20 : 24;
       mbar_init(&t.bars[i], n);
     }
@@ -864,11 +937,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   if (warp < kMaskWarp) {
     set_regs_dec<40>();
     if (warp == kLoadWarp)
-      load_role<NT, PAIR, PL>(t, a, &tq, &tk, &tv, h0);
-    else if (warp == kMmaWarp)
-      mma_role<NT, PAIR, PL>(t, a, withhold);
-    else if (warp - kGateWarp < L::kHeads)
-      gate_role<NT, PAIR, PL>(t, a, h0 + warp - kGateWarp, warp - kGateWarp, u);
+      load_role<NT, PAIR, PL>(t, a, &tq, &tk, &tv, h0, withhold);
+    else if (warp == kDsWarp)
+      ds_role<NT, PAIR, PL>(t, a);
+    else if (warp == kGateWarp)
+      gate_role<NT, PAIR, PL>(t, a, h0, u);
+    else if (warp == kYWarp && !a.states_only)
+      y_role<NT, PAIR, PL>(t, a);
   } else if (warp < kDecayWarp) {
     set_regs_dec<56>();
     mask_role<NT, PAIR, PL>(t, a);
@@ -917,9 +992,11 @@ cudaError_t launch_one(const LaPass& p, cudaStream_t st) {
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
+  // a poll takes 1 us (2000 cycles) at most: the bound in polls is within that of the wait limit
+  const uint32_t polls = (uint32_t)std::min<long long>(std::max<long long>(device_wait_limit() / 2000, 1), 1u << 22);
   const int64_t units = p.segmented ? p.max_windows : p.nseq;
   fn<<<(unsigned)(units * (PAIR ? p.H / 2 : p.H)), kThreadsTc, L::kBytes, st>>>(
-      tq, tk, tv, p, device_status_word(), device_wait_limit(), device_withhold() & 4);
+      tq, tk, tv, p, device_status_word(), polls, device_withhold() & 4);
   count_launches(1);
   return cudaGetLastError();
 }
