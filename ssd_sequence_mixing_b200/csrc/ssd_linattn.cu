@@ -543,23 +543,48 @@ __global__ void __launch_bounds__(1024) la_table_kernel(int64_t tokens, int nseq
 }
 
 // carry[w] holds window w's own end state (from zero; the first window's from `start`) and
-// becomes the state that window w starts from.  One thread per state element, sequence and
-// head: a read and a write of 4 bytes per window, bound by HBM.
+// becomes the state that window w starts from.  One thread per V (1 or 4 elements) of a state; the
+// loads of 8 windows are in flight together (one after another, each behind the last one's
+// store, took 130 us for 64 states of 8 windows, and these 20).  A read and a write of every
+// state but the last: bound by HBM.
+template <typename V>
 __global__ void __launch_bounds__(256) la_scan_kernel(LaPass a) {
   if (a.win_count && *a.win_count < 0) return;
+  constexpr int kV = sizeof(V) / sizeof(float), kBatch = 8;
   const int64_t sh = blockIdx.x;
   const int seq = (int)(sh / a.H), h = (int)(sh % a.H);
   const int64_t size = (int64_t)a.PV * a.NK;
   const int w0 = a.cu ? a.first_win[seq] : seq * a.dense_windows;
   const int n = a.cu ? a.first_win[seq + 1] - w0 : a.dense_windows;
-  for (int64_t e = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; e < size; e += (int64_t)gridDim.y * blockDim.x) {
-    float state = 0.f;
-    for (int i = 0; i < n; ++i) {
-      const int64_t w = w0 + (a.reverse ? n - 1 - i : i);
-      float* p = a.carry + (w * a.H + h) * size + e;
-      const float own = i + 1 < n ? *p : 0.f;  // the last one's is not computed
-      if (i > 0) *p = state;                    // the first one starts from `start`
-      state = i > 0 ? fmaf(state, i + 1 < n ? a.window_decay[w * a.H + h] : 0.f, own) : own;
+  const int64_t e = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * kV;
+  if (e >= size) return;
+  const int64_t pitch = (a.reverse ? -1 : 1) * a.H * size;  // from a window to the next in order
+  float* p = a.carry + ((int64_t)(a.reverse ? w0 + n - 1 : w0) * a.H + h) * size + e;
+  const float* decay = a.window_decay + (int64_t)(a.reverse ? w0 + n - 1 : w0) * a.H + h;
+  const int64_t dpitch = (a.reverse ? -1 : 1) * a.H;
+  alignas(16) float state[kV];
+#pragma unroll
+  for (int k = 0; k < kV; ++k) state[k] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    alignas(16) float own[kBatch][kV];
+    float dec[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const bool in = i0 + i + 1 < n;  // the last window's own state is not computed
+      dec[i] = in && i0 + i > 0 ? decay[(i0 + i) * dpitch] : 0.f;
+      if (in) {
+        *reinterpret_cast<V*>(own[i]) = *reinterpret_cast<const V*>(p + (i0 + i) * pitch);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kV; ++k) own[i][k] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      // the first window starts from `start` itself
+      if (i0 + i > 0 && i0 + i < n) *reinterpret_cast<V*>(p + (i0 + i) * pitch) = *reinterpret_cast<const V*>(state);
+#pragma unroll
+      for (int k = 0; k < kV; ++k) state[k] = i0 + i > 0 ? fmaf(state[k], dec[i], own[i][k]) : own[i][k];
     }
   }
 }
@@ -600,8 +625,12 @@ cudaError_t launch_la_general(const LaPass& p, bool bf16, bool exact, cudaStream
 
 cudaError_t launch_la_scan(const LaPass& p, cudaStream_t st) {
   const int64_t size = (int64_t)p.PV * p.NK;
-  const dim3 grid((unsigned)((int64_t)p.nseq * p.H), (unsigned)((size + 1023) / 1024));
-  la_scan_kernel<<<grid, 256, 0, st>>>(p);
+  const bool vec = size % 4 == 0;
+  const dim3 grid((unsigned)((int64_t)p.nseq * p.H), (unsigned)((size / (vec ? 4 : 1) + 255) / 256));
+  if (vec)
+    la_scan_kernel<float4><<<grid, 256, 0, st>>>(p);
+  else
+    la_scan_kernel<float><<<grid, 256, 0, st>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }

@@ -123,18 +123,19 @@ __device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&r)[16]) {
       : "r"(t)
       : "memory");
 }
-// 16 lanes x 32 columns in the layout of mma.sync's accumulators: registers 4 t .. 4 t + 3 are
+// 16 lanes x 16 (8) columns in the layout of mma.sync's accumulators: registers 4 t .. 4 t + 3 are
 // columns 8 t + 2 (lane % 4), + 1 of row lane / 4, then of row lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_16x256_x4(uint32_t t, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(t)
-      : "memory");
+__device__ __forceinline__ void tmem_ld_16x256_x1(uint32_t t, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(t)
+               : "memory");
 }
-// The same for 16 columns.
+__device__ __forceinline__ void tmem_st_16x256_x1(uint32_t t, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t t, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -596,10 +597,62 @@ __device__ __forceinline__ void decay_role(const Cta& t, const LaPass& a) {
   }
 }
 
-// Writes the thread's part of the state, element n of its row to to[n * step]: through the columns
-// of dS in tensor memory (which no product uses at that time), so that a small loop does it.
+// Where a state lies in memory: element (r, n) of the head at base + r * sr + n * sc.
+struct StateAt {
+  float* base;
+  int64_t sr, sc;
+};
+
+// Moves the warp's 32 rows from row0 and NC columns from n0 between memory and the columns of dS
+// in tensor memory (`ds`; no product uses them at that time), in small loops.  Rows are
+// contiguous in memory (sc = 1: 8 rows x 32 bytes an access) or columns are (a lane per row).
+template <int NC, bool STORE>
+__device__ __forceinline__ void move_state(uint32_t ds, const StateAt& at, int lane, int row0, int n0, int rows, int cols) {
+  if (at.sc == 1) {
+    const int r0 = row0 + (lane >> 2), c0 = n0 + 2 * (lane & 3);
+#pragma unroll 1
+    for (int i = 0; i < NC / 4; ++i) {  // 8 columns, half of the rows
+      const int r = r0 + 16 * (i & 1), n = 8 * (i >> 1);
+      const uint32_t t = ds + ((uint32_t)(16 * (i & 1)) << 16) + n;
+      float* p = at.base + r * at.sr + c0 + n;
+      const bool in = c0 + n < cols, lo = in && r < rows, hi = in && r + 8 < rows;  // (both even)
+      uint32_t v[4] = {0u, 0u, 0u, 0u};
+      if (STORE) {
+        tmem_ld_16x256_x1(t, v);
+        tmem_ld_wait();
+        if (lo) *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
+        if (hi) *reinterpret_cast<uint2*>(p + 8 * at.sr) = make_uint2(v[2], v[3]);
+      } else {
+        if (lo) *reinterpret_cast<uint2*>(&v[0]) = *reinterpret_cast<const uint2*>(p);
+        if (hi) *reinterpret_cast<uint2*>(&v[2]) = *reinterpret_cast<const uint2*>(p + 8 * at.sr);
+        tmem_st_16x256_x1(t, v);
+      }
+    }
+  } else {
+    float* p = at.base + (row0 + lane) * at.sr + n0 * at.sc;
+#pragma unroll 1
+    for (int n = 0; n < NC; n += 8) {
+      uint32_t v[8];
+      if (STORE) {
+        tmem_ld8(ds + n, v);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = row0 + lane < rows && n0 + n + i < cols;
+        if (!STORE)
+          v[i] = in ? __float_as_uint(p[(n + i) * at.sc]) : 0u;
+        else if (in)
+          p[(n + i) * at.sc] = __uint_as_float(v[i]);
+      }
+      if (!STORE) tmem_st8(ds + n, v);
+    }
+  }
+  if (!STORE) tmem_st_wait();
+}
 template <int NC>
-__device__ __forceinline__ void put_state(uint32_t ds, const float (&S)[NC], float* to, int64_t step, int count, bool mine) {
+__device__ __forceinline__ void put_state(uint32_t ds, const float (&S)[NC], const StateAt& at, int lane, int row0, int n0,
+                                          int rows, int cols) {
 #pragma unroll
   for (int b = 0; b < NC / 16; ++b) {
     uint32_t v[16];
@@ -608,15 +661,7 @@ __device__ __forceinline__ void put_state(uint32_t ds, const float (&S)[NC], flo
     tmem_st16(ds + 16 * b, v);
   }
   tmem_st_wait();
-#pragma unroll 1
-  for (int n = 0; n < NC; n += 8) {
-    uint32_t v[8];
-    tmem_ld8(ds + n, v);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (mine && n + i < count) to[(n + i) * step] = __uint_as_float(v[i]);
-  }
+  move_state<NC, true>(ds, at, lane, row0, n0, rows, cols);
 }
 
 // Plane p of the state that step c's outputs see, to tensor memory.
@@ -659,32 +704,24 @@ __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const 
   constexpr int NC = NT / 2, sp_slots = PAIR ? 1 : 2;  // columns of a thread
   const int w = threadIdx.x / 32 - kStateWarp, q = w & 3, half = w >> 2;
   const int head = PAIR ? q >> 1 : 0, h = h0 + head;
-  const int r = PAIR ? (32 * q & 63) + t.lane : 32 * q + t.lane;  // value row of the head
-  const bool active = r - t.lane < a.PV, mine = r < a.PV;
+  const int row0 = PAIR ? 32 * q & 63 : 32 * q;  // the warp's first row of the head
+  const bool active = row0 < a.PV;
   const int n0 = half * NC;
   const bool begins = a.reverse ? un.last : un.first, ends = a.reverse ? un.first : un.last;
   const uint32_t lanes = (uint32_t)(32 * q) << 16;
   const int64_t state_at = ((int64_t)un.seq * a.H + h) * a.NK * a.PV;
   const uint32_t ds = t.tmem + lanes + kColDs + n0;  // the thread's part of dS
-  const int count = max(0, min(NC, a.NK - n0));
-  auto window_at = [&](float* base, int64_t win) { return base + ((win * a.H + h) * a.PV + r) * a.NK + n0; };
+  auto window_at = [&](float* base, int64_t win) {
+    return StateAt{base + (win * a.H + h) * a.PV * a.NK, (int64_t)a.NK, 1};
+  };
   float S[NC];
   {
-    const float* from = nullptr;
-    int64_t step = 1;
-    if (begins) {
-      if (a.start) from = a.start + state_at + r * a.sr + n0 * a.sc, step = a.sc;
-    } else if (!a.states_only) {
+    StateAt from{nullptr, a.NK, 1};
+    if (!begins && !a.states_only)
       from = window_at(a.carry, u);
-    }
-#pragma unroll 1
-    for (int n = 0; n < NC; n += 8) {
-      uint32_t v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = from && mine && n + i < count ? __float_as_uint(from[(n + i) * step]) : 0u;
-      tmem_st8(ds + n, v);
-    }
-    tmem_st_wait();
+    else if (begins && a.start)
+      from = StateAt{const_cast<float*>(a.start) + state_at, a.sr, a.sc};
+    move_state<NC, false>(ds, from, t.lane, row0, n0, from.base ? a.PV : 0, a.NK);
 #pragma unroll
     for (int b = 0; b < NC / 16; ++b) {
       uint32_t v[16];
@@ -697,7 +734,7 @@ __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const 
   // windows whose state is wanted: forward, after the window's last block; reverse, before it
   auto wanted = [&](int ci) { return a.dump && (ci == t.chunks - 1 || (ci + 1) * kC % a.window == 0); };
   auto dump_at = [&](int ci) { return window_at(a.dump, un.first_window + ci * kC / a.window); };
-  if (a.reverse && t.chunks && wanted(t.chunks - 1)) put_state<NC>(ds, S, dump_at(t.chunks - 1), 1, count, mine);
+  if (a.reverse && t.chunks && wanted(t.chunks - 1)) put_state<NC>(ds, S, dump_at(t.chunks - 1), t.lane, row0, n0, a.PV, a.NK);
   tc_fence_before();
   t.arrive(kDsFree);
   if (!a.states_only && t.chunks)
@@ -726,7 +763,7 @@ __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const 
       if (more) tmem_st8(sp + 8 * b, v);
     }
     const int at = a.reverse ? ci - 1 : ci;  // the block whose window's state this may be
-    if (at >= 0 && wanted(at)) put_state<NC>(ds, S, dump_at(at), 1, count, mine);
+    if (at >= 0 && wanted(at)) put_state<NC>(ds, S, dump_at(at), t.lane, row0, n0, a.PV, a.NK);
     tc_fence_before();
     t.arrive(kDsFree);
     t.arrive(kGFree + c % kGateSlots);
@@ -740,9 +777,9 @@ __device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const 
     }
   }
   if (a.states_only)
-    put_state<NC>(ds, S, window_at(a.carry, u), 1, count, mine);
+    put_state<NC>(ds, S, window_at(a.carry, u), t.lane, row0, n0, a.PV, a.NK);
   else if (a.last && ends)
-    put_state<NC>(ds, S, a.last + state_at + r * a.sr + n0 * a.sc, a.sc, count, mine);
+    put_state<NC>(ds, S, StateAt{a.last + state_at, a.sr, a.sc}, t.lane, row0, n0, a.PV, a.NK);
 }
 
 // Yi, Ya -> out: warp q writes rows 32 q .., 16 tokens at a time.  Tensor memory is read in the layout of mma.sync's accumulators (registers are pairs of
