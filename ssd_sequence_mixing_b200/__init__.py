@@ -159,7 +159,7 @@ def library() -> ctypes.CDLL:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _io_code(dtype: torch.dtype) -> int:
@@ -187,6 +187,9 @@ def make_shape(x: torch.Tensor, B: torch.Tensor, cu_seqlens=None, cu_seqlens_hos
 
 def _check(name, t, device, dtype=None, shape=None):
     if t is None:
+        return
+    if (t.device == device and (dtype is None or t.dtype == dtype) and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
         return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -469,9 +472,19 @@ def ssd_decode_step(x, dt, A, B, C, D, state, y: Optional[torch.Tensor] = None, 
 
 
 def _handle(stream, device):
+    """The raw handle of ``stream``, by default torch's current one on ``device`` (asked for as
+    torch's own generated code does: a torch.cuda.Stream object costs 2 us)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_device(call, device, *args):
+    """The library's call with ``device`` current (the usual case needs no switch)."""
+    if torch.cuda.current_device() == device.index:
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
 
 
 def _attention_shape(q, k, v, log_decay, cu_seqlens, cu_seqlens_host):
@@ -530,10 +543,7 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         final_state = torch.empty(states, dtype=torch.float32, device=device)
     _check("final_state", final_state, device, torch.float32, states)
     scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
-    with torch.cuda.device(device):
-        rc = _lib.ssd_linear_attention_forward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                               int(per_token), scale, _ptr(init_state), _ptr(cu_seqlens), _ptr(y),
-                                               _ptr(final_state), _handle(stream, device))
+    rc = _on_device(_lib.ssd_linear_attention_forward, device, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), scale, _ptr(init_state), _ptr(cu_seqlens), _ptr(y), _ptr(final_state), _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_linear_attention_forward")
     return y, final_state
@@ -561,11 +571,7 @@ def linear_attention_backward(dy: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     dlog = torch.empty_like(log_decay) if need_dlog_decay else None
     dinit = torch.empty(states, dtype=torch.float32, device=device) if init_state is not None else None
     scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
-    with torch.cuda.device(device):
-        rc = _lib.ssd_linear_attention_backward(ctypes.byref(shape), _ptr(dy), _ptr(q), _ptr(k), _ptr(v),
-                                                _ptr(log_decay), int(per_token), scale, _ptr(init_state),
-                                                _ptr(dfinal_state), _ptr(cu_seqlens), _ptr(dq), _ptr(dk), _ptr(dv),
-                                                _ptr(dlog), _ptr(dinit), _handle(stream, device))
+    rc = _on_device(_lib.ssd_linear_attention_backward, device, ctypes.byref(shape), _ptr(dy), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), scale, _ptr(init_state), _ptr(dfinal_state), _ptr(cu_seqlens), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlog), _ptr(dinit), _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_linear_attention_backward")
     return dq, dk, dv, dlog, dinit
@@ -586,9 +592,7 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
         y = torch.empty_like(v)
     _check("y", y, device, v.dtype, tuple(v.shape))
     scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
-    with torch.cuda.device(device):
-        rc = _lib.ssd_linear_attention_step(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                            int(per_row), scale, _ptr(state), _ptr(y), _handle(stream, device))
+    rc = _on_device(_lib.ssd_linear_attention_step, device, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_row), scale, _ptr(state), _ptr(y), _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_linear_attention_step")
     return y
@@ -615,10 +619,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     count = beams if count is None else int(count)
     out = torch.empty((batch, count), dtype=torch.float32, device=device)
     tokens, parents = (torch.empty((batch, count), dtype=torch.int32, device=device) for _ in range(2))
-    with torch.cuda.device(device):
-        rc = _lib.ssd_beam_select(batch, beams, vocab, _io_code(logits.dtype), _ptr(logits), _ptr(scores),
-                                  _ptr(finished), int(eos), count, _ptr(out), _ptr(tokens), _ptr(parents),
-                                  _handle(stream, device))
+    rc = _on_device(_lib.ssd_beam_select, device, batch, beams, vocab, _io_code(logits.dtype), _ptr(logits), _ptr(scores), _ptr(finished), int(eos), count, _ptr(out), _ptr(tokens), _ptr(parents), _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_beam_select")
     return out, tokens, parents
@@ -647,8 +648,7 @@ def state_reorder(states, parents: torch.Tensor, stream=None) -> None:
     rows = max(1, batch * beams)
     ptrs = (ctypes.c_void_p * max(1, n))(*[s.data_ptr() for s in states])
     sizes = (ctypes.c_int64 * max(1, n))(*[s.numel() // rows * s.element_size() for s in states])
-    with torch.cuda.device(device):
-        rc = _lib.ssd_state_reorder(batch, beams, _ptr(parents), n, ptrs, sizes, _handle(stream, device))
+    rc = _on_device(_lib.ssd_state_reorder, device, batch, beams, _ptr(parents), n, ptrs, sizes, _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_state_reorder")
 

@@ -78,7 +78,8 @@ int la_general_slices(int PV);
 // The tcgen05 kernel (bf16): whether it takes the pass, and whether its CTAs take two heads each.
 bool la_tc_supports(const LaPass& p);
 bool la_tc_pairs(const LaPass& p);
-cudaError_t launch_la_tc(const LaPass& p, bool exact, cudaStream_t st);
+// Up to three passes of one problem, side by side; a pass with `dots` keeps fp32 accuracy.
+cudaError_t launch_la_tc(const LaPass* p, int passes, cudaStream_t st);
 // carry[w] <- the state before window w (reverse: after it in time), from the windows' own states.
 cudaError_t launch_la_scan(const LaPass& p, cudaStream_t st);
 

@@ -294,27 +294,37 @@ Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, int64_t res
 bool wants_tc(const ssd_shape* s) {
   return s->io_dtype == SSD_BF16 && s->headdim % 8 == 0 && s->dstate % 8 == 0 && path_setting() != SSD_PATH_SIMT;
 }
-Plan plan_for(const ssd_shape* s, const int32_t* cu, bool tc, bool pairs, int slices) {
-  return tc ? make_plan(s, cu, pairs ? s->nheads / 2 : s->nheads, device_sm_count())
-            : make_plan(s, cu, s->nheads * slices, 3 * (int64_t)device_sm_count());
+Plan plan_for(const ssd_shape* s, const int32_t* cu, bool tc, int64_t lanes) {
+  return make_plan(s, cu, lanes, (tc ? 1 : 3) * (int64_t)device_sm_count());
 }
 
-// One pass: the windows' states first where it is segmented.
-cudaError_t run_pass(LaPass p, bool tc, bool bf16, bool exact, float* carry, float* window_decay, cudaStream_t st) {
-  p.carry = carry;
-  p.window_decay = window_decay;
-  auto launch = [&](const LaPass& q, bool ex) {
-    return tc && la_tc_supports(q) ? launch_la_tc(q, ex, st) : launch_la_general(q, bf16, ex, st);
-  };
-  if (p.segmented) {
-    LaPass own = p;
-    own.states_only = 1;
-    own.dump = nullptr, own.last = nullptr, own.dot = nullptr;
-    cudaError_t e = launch(own, false);
-    if (e == cudaSuccess) e = launch_la_scan(p, st);
-    if (e != cudaSuccess) return e;
+// Passes over one problem, with the windows' states first where it is segmented: side by side in
+// one launch on the tcgen05 kernel (a batch that gives one pass too few CTAs may fill the GPU with
+// three), one after another on the general one.  Pass i has the i-th part of carry and
+// window_decay to itself.
+cudaError_t run_passes(LaPass* p, int n, bool tc, bool bf16, float* carry, float* window_decay, cudaStream_t st) {
+  const LaPass& q = p[0];
+  const size_t states = (size_t)q.max_windows * q.H * q.NK * q.PV, decays = (size_t)q.max_windows * q.H;
+  LaPass own[3];
+  for (int i = 0; i < n; ++i) {
+    p[i].carry = carry + i * states;
+    p[i].window_decay = window_decay + i * decays;
+    own[i] = p[i];
+    own[i].states_only = 1;
+    own[i].dump = nullptr, own[i].last = nullptr, own[i].dot = nullptr, own[i].dots = nullptr, own[i].out_f32 = 0;
   }
-  return launch(p, exact);
+  auto launch = [&](const LaPass* l) {
+    if (tc && la_tc_supports(l[0])) return launch_la_tc(l, n, st);
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_la_general(l[i], bf16, l[i].dots != nullptr, st);
+    return e;
+  };
+  cudaError_t e = cudaSuccess;
+  if (q.segmented) {
+    e = launch(own);
+    for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_la_scan(p[i], st);
+  }
+  return e == cudaSuccess ? launch(p) : e;
 }
 
 struct TableLayout {
@@ -376,7 +386,7 @@ extern "C" int ssd_linear_attention_forward(const ssd_shape* s, const void* q, c
   const int P = (int)s->headdim, N = (int)s->dstate, H = (int)s->nheads, hpg = (int)(s->nheads / s->ngroups);
   const bool tc = wants_tc(s);
   if (path_setting() == SSD_PATH_TC && !tc) return SSD_ERR_UNSUPPORTED;
-  const Plan plan = plan_for(s, cu, tc, P <= 64 && hpg % 2 == 0, la_general_slices(P));
+  const Plan plan = plan_for(s, cu, tc, tc ? (P <= 64 && hpg % 2 == 0 ? H / 2 : H) : H * la_general_slices(P));
   const TableLayout tl(plan, rows, 0);
   const size_t o_carry = tl.total;
   const size_t o_dec = o_carry + (plan.segmented ? up256(sizeof(float) * (size_t)plan.max_windows * H * P * N) : 0);
@@ -393,7 +403,7 @@ extern "C" int ssd_linear_attention_forward(const ssd_shape* s, const void* q, c
   p.out = y;
   const bool bf16 = s->io_dtype == SSD_BF16;
   cudaError_t e = build_table(s, plan, cu, ws, tl, status, st);
-  if (e == cudaSuccess) e = run_pass(p, tc, bf16, false, (float*)(ws + o_carry), (float*)(ws + o_dec), st);
+  if (e == cudaSuccess) e = run_passes(&p, 1, tc, bf16, (float*)(ws + o_carry), (float*)(ws + o_dec), st);
   const cudaError_t e2 = ws ? cudaFreeAsync(ws, st) : cudaSuccess;
   return e != cudaSuccess || e2 != cudaSuccess ? SSD_ERR_CUDA : SSD_OK;
 }
@@ -425,7 +435,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
   if (path_setting() == SSD_PATH_TC && !tc) return SSD_ERR_UNSUPPORTED;
   const int slices = std::min(la_general_slices(P), la_general_slices(N));
   const int dot_slices = tc && tokens > 0 ? (N + 31) / 32 : la_general_slices(N);  // partial dots of a token
-  const Plan plan = plan_for(s, cu, tc, false, slices);
+  const Plan plan = plan_for(s, cu, tc, tc ? 3 * H : H * slices);
   const size_t W = (size_t)plan.max_windows, state = (size_t)H * P * N, th = (size_t)tokens * H;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -435,12 +445,12 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
   };
   const TableLayout tl(plan, rows, 0);
   at = tl.total;
-  const size_t o_carry = take(plan.segmented ? 4 * W * state : 0);
-  const size_t o_dec = take(plan.segmented ? 4 * W * H : 0);
+  const size_t o_carry = take(plan.segmented ? 3 * 4 * W * state : 0);
+  const size_t o_dec = take(plan.segmented ? 3 * 4 * W * H : 0);
   const size_t o_send = take(decay_grad ? 4 * W * state : 0), o_dend = take(decay_grad ? 4 * W * state : 0);
   const size_t o_qdot = take(decay_grad ? 4 * th * dot_slices : 0), o_kdot = take(decay_grad ? 4 * th * dot_slices : 0);
   const size_t o_parts = take(decay_grad && !decay_per_token ? 8 * W * H : 0);
-  const size_t o_part = take(shared ? 4 * th * N : 0);
+  const size_t o_dq = take(shared ? 4 * th * N : 0), o_dk = take(shared ? 4 * th * N : 0);
   char* ws = nullptr;
   if (at && scratch_alloc((void**)&ws, at, st) != cudaSuccess) return SSD_ERR_CUDA;
   float *carry = (float*)(ws + o_carry), *dec = (float*)(ws + o_dec);
@@ -449,49 +459,46 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
 
   LaPass base{};
   set_common(base, s, plan, cu, ws, tl, log_decay, decay_per_token, scale);
-  auto group_sum = [&](void* dst) {
-    const int64_t n = tokens * G * N;
-    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 148 * 32);
-    if (n == 0) return cudaSuccess;
-    if (bf16)
-      la_group_sum_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>((const float*)(ws + o_part), (__nv_bfloat16*)dst, n, N, hpg, count);
-    else
-      la_group_sum_kernel<float><<<blocks, 256, 0, st>>>((const float*)(ws + o_part), (float*)dst, n, N, hpg, count);
-    count_launches(1);
-    return cudaGetLastError();
-  };
-  if (e == cudaSuccess) {  // dq = pass (dy, v, k) from init^T
-    LaPass p = base;
+  LaPass pass[3] = {base, base, base};
+  {  // dq = pass (dy, v, k) from init^T
+    LaPass& p = pass[0];
     p.query = dy, p.key = v, p.value = k;
     p.q_heads = p.k_heads = H, p.v_heads = G, p.q_div = p.k_div = 1, p.v_div = hpg;
     p.NK = P, p.PV = N;
     p.start = init_state, p.sr = 1, p.sc = N;
-    p.out = shared ? (void*)(ws + o_part) : dq, p.out_f32 = shared;
+    p.out = shared ? (void*)(ws + o_dq) : dq, p.out_f32 = shared;
     if (decay_grad) p.dump = (float*)(ws + o_send), p.dot = q, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_qdot);
-    e = run_pass(p, tc, bf16, decay_grad, carry, dec, st);
-    if (e == cudaSuccess && shared) e = group_sum(dq);
   }
-  if (e == cudaSuccess) {  // dk = pass (v, dy, q), backwards from dfinal^T
-    LaPass p = base;
+  {  // dk = pass (v, dy, q), backwards from dfinal^T
+    LaPass& p = pass[1];
     p.reverse = 1;
     p.query = v, p.key = dy, p.value = q;
     p.q_heads = p.k_heads = H, p.v_heads = G, p.q_div = p.k_div = 1, p.v_div = hpg;
     p.NK = P, p.PV = N;
     p.start = dfinal_state, p.sr = 1, p.sc = N;
-    p.out = shared ? (void*)(ws + o_part) : dk, p.out_f32 = shared;
+    p.out = shared ? (void*)(ws + o_dk) : dk, p.out_f32 = shared;
     if (decay_grad) p.dump = (float*)(ws + o_dend), p.dot = k, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_kdot);
-    e = run_pass(p, tc, bf16, decay_grad, carry, dec, st);
-    if (e == cudaSuccess && shared) e = group_sum(dk);
   }
-  if (e == cudaSuccess) {  // dv = pass (k, q, dy), backwards from dfinal; its last state is dinit
-    LaPass p = base;
+  {  // dv = pass (k, q, dy), backwards from dfinal; its last state is dinit
+    LaPass& p = pass[2];
     p.reverse = 1;
     p.query = k, p.key = q, p.value = dy;
     p.q_heads = p.k_heads = G, p.v_heads = H, p.q_div = p.k_div = hpg, p.v_div = 1;
     p.NK = N, p.PV = P;
     p.start = dfinal_state, p.last = dinit_state, p.sr = N, p.sc = 1;
     p.out = dv;
-    e = run_pass(p, tc, bf16, false, carry, dec, st);
+  }
+  if (e == cudaSuccess) e = run_passes(pass, 3, tc, bf16, carry, dec, st);
+  for (int i = 0; i < 2 && e == cudaSuccess && shared && tokens > 0; ++i) {
+    const int64_t n = tokens * G * N;
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 148 * 32);
+    const float* src = (const float*)(ws + (i ? o_dk : o_dq));
+    if (bf16)
+      la_group_sum_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(src, (__nv_bfloat16*)(i ? dk : dq), n, N, hpg, count);
+    else
+      la_group_sum_kernel<float><<<blocks, 256, 0, st>>>(src, (float*)(i ? dk : dq), n, N, hpg, count);
+    count_launches(1);
+    e = cudaGetLastError();
   }
   if (e == cudaSuccess && decay_grad) {
     LaGrad g{};

@@ -55,9 +55,9 @@ using namespace sm100;
 
 constexpr int kC = kLaChunk;  // tokens of a block
 constexpr int kAtomBytes = kC * 128;  // 64 tokens x 64 columns of bf16, 128-byte rows
-constexpr int kMaxStages = 3, kGateSlots = 4, kPlanes = 3;
+constexpr int kMaxStages = 3, kGateSlots = 4, kPlanes = 3, kUnitSlots = 4;
 constexpr int kWarpsTc = 28, kThreadsTc = 32 * kWarpsTc;
-constexpr int kLoadWarp = 0, kDsWarp = 1, kGateWarp = 2, kYWarp = 3, kMaskWarp = 4, kDecayWarp = 8, kStateWarp = 16, kOutWarp = 24;
+constexpr int kLoadWarp = 0, kDsWarp = 1, kGateWarp = 2, kMaskWarp = 4, kDecayWarp = 8, kStateWarp = 16, kOutWarp = 24;
 
 // tensor memory columns
 constexpr int kColS1 = 0, kColYi = 64, kColYa = 128, kColDs = 256, kColUv = 384, kColSp0 = 448, kColSp1 = 192;
@@ -75,8 +75,21 @@ enum Bar {
   kSpFull, kSpFree = kSpFull + 2,
   kYFull = kSpFree + 2, kYFree,
   kGFull, kGFree = kGFull + kGateSlots,
-  kDrain = kGFree + kGateSlots,  // every product of a warp that issues them is done
-  kBars = kDrain + 3
+  kUnit = kGFree + kGateSlots, kUnitFree = kUnit + kUnitSlots,  // a unit's description
+  kDrain = kUnitFree + kUnitSlots,  // every product of a warp that issues them is done
+  kBars = kDrain + 2
+};
+
+// A unit as its CTA's roles see it, in shared memory; chunks < 0: there is none left.
+struct alignas(16) UnitDesc {
+  LaPass a;
+  Unit un;
+  int u, h0, chunks, planes, pass;
+  int begins, ends;
+  // The block processed at step c: its place in the unit, its first token and its tokens.
+  __device__ __forceinline__ int block(int c) const { return a.reverse ? chunks - 1 - c : c; }
+  __device__ __forceinline__ int64_t token(int c) const { return un.t0 + (int64_t)block(c) * kC; }
+  __device__ __forceinline__ int rows(int c) const { return min(kC, un.len - block(c) * kC); }
 };
 
 struct Gate {
@@ -100,7 +113,8 @@ struct TcSmem {
   static constexpr int kDot = kOut + 4 * kOutBytes;                              // ... rows to multiply them with
   static constexpr int kBar = kDot + 4 * kDotBytes;
   static constexpr int kFlag = kBar + 8 * kBars;
-  static constexpr int kBytes = kFlag + 16 + 1024;                  // 1024: alignment of the base
+  static constexpr int kUnits = (kFlag + 4 + 15) / 16 * 16;
+  static constexpr int kBytes = kUnits + kUnitSlots * (int)sizeof(UnitDesc) + 1024;                  // 1024: alignment of the base
 };
 
 __device__ __forceinline__ void tmem_ld8(uint32_t t, uint32_t (&r)[8]) {
@@ -190,6 +204,19 @@ __device__ __forceinline__ float exp2_split(double c, float& hi, float& lo) {
   return ex2(lo) * (whole < -126 ? 0.f : __int_as_float((whole + 127) << 23));
 }
 
+// One launch: up to three passes, each over its units (sequences or windows, times heads or pairs
+// of heads), walked by a CTA per SM.
+struct TcWork {
+  int passes, total;   // total: units of all passes
+  int first[4];        // first unit of each pass
+  int exact[3];        // the pass wants P and S in three planes
+  int8_t map[3][3];    // tensor maps of its query, key and value
+  LaPass pass[3];
+};
+struct TcMaps {
+  CUtensorMap m[4];
+};
+
 // What every role needs.
 struct Cta {
   uint8_t* smem;
@@ -197,9 +224,7 @@ struct Cta {
   volatile int* abort_flag;
   uint32_t polls;
   uint32_t tmem;
-  int chunks;
-  int64_t t0;
-  int len, lane;
+  int lane;
   // A whole warp waits for the n-th completion of a barrier (n from 0).  A wait that gives up
   // ends the role; the others' waits run out in turn.
   __device__ __forceinline__ bool wait(int bar, int n) const {
@@ -215,12 +240,30 @@ struct Cta {
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[bar]);
   }
-  // The block processed at step c: its first token and its tokens.
-  __device__ __forceinline__ int64_t token(const LaPass& a, int c) const {
-    return t0 + (int64_t)(a.reverse ? chunks - 1 - c : c) * kC;
+};
+
+// A role's place in the CTA's list of units, which the load warp makes.  Blocks are numbered
+// through all of it (`g` in the roles), which is what the barriers' phases go by.
+struct Units {
+  const Cta& t;
+  const UnitDesc* ring;
+  const UnitDesc* d;
+  int n;
+  __device__ __forceinline__ Units(const Cta& cta, int off)
+      : t(cta), ring(reinterpret_cast<const UnitDesc*>(cta.smem + off)), d(nullptr), n(-1) {}
+  __device__ __forceinline__ bool next() {
+    if (n >= 0) t.arrive(kUnitFree + n % kUnitSlots);
+    ++n;
+    if (!t.wait(kUnit + n % kUnitSlots, n / kUnitSlots)) return false;
+    d = ring + n % kUnitSlots;
+    return d->chunks >= 0;
   }
-  __device__ __forceinline__ int rows(const LaPass& a, int c) const {
-    return min(kC, len - (a.reverse ? chunks - 1 - c : c) * kC);
+  // The same without giving the last one back (for a second walk of one role).
+  __device__ __forceinline__ bool peek() {
+    ++n;
+    if (!t.wait(kUnit + n % kUnitSlots, n / kUnitSlots)) return false;
+    d = ring + n % kUnitSlots;
+    return true;
   }
 };
 
@@ -247,79 +290,103 @@ struct Issue {
   }
 };
 
-// Tiles by TMA, and S1 of each block.
+// Tiles by TMA.
 template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void load_role(const Cta& t, const LaPass& a, const CUtensorMap* tq, const CUtensorMap* tk,
-                                          const CUtensorMap* tv, int h0, int withhold) {
+__device__ __forceinline__ void load_role(const Cta& t, const TcWork& work, const TcMaps& maps) {
   using L = TcSmem<NT, PAIR, PL>;
-  const Issue mma(t);
-  const int qh = h0 / a.q_div, kh = h0 / a.k_div, vh = h0 / a.v_div;  // (two heads: v_div is 1)
-  const int v_atoms = PAIR || a.PV > 64 ? 2 : 1;
-  const uint32_t bytes = ((a.states_only ? 1 : 2) * (NT / 64) + v_atoms) * kAtomBytes;
-  constexpr uint32_t id_s1 = idesc_bf16(64, kC, 0, 0);
-  constexpr int kAhead = L::kStages - 1;  // blocks loaded before they are needed
-  bool ok = true;
-  int s = 0, use = 0, ls = 0, luse = 0;  // stage and its use: of the products, of the loads
+  UnitDesc* ring = reinterpret_cast<UnitDesc*>(t.smem + L::kUnits);
+  int s = 0, use = 0;  // stage, and its use
+  bool ok = true, left = true;
 #pragma unroll 1
-  for (int c = -kAhead; c < t.chunks; ++c) {
-    if (c >= 0 && !a.states_only) {
-      // the tiles as they landed: what a last block holds past its end is masked in P
-      if (!(ok = t.wait(kFull + s, use)) || !(ok = t.wait_free(kS1Free, c))) break;
-      tc_fence_after();
-      if (mma.leader) {
-        const uint64_t q = mma.at(mma.k_major, s * L::kStage + L::kQ), k = mma.at(mma.k_major, s * L::kStage + L::kK);
+  for (int n = 0, w = (int)blockIdx.x; ok && left; w += (int)gridDim.x) {
+    // the next unit that has work
+    left = w < work.total;
+    const int pass = left ? (work.passes > 1 && w >= work.first[1]) + (work.passes > 2 && w >= work.first[2]) : 0;
+    UnitDesc* d = ring + n % kUnitSlots;
+    int h0 = 0, chunks = -1;
+    Unit un{};
+    if (left) {
+      const LaPass& a = work.pass[pass];
+      const int rel = w - work.first[pass], per = a.H / L::kHeads;
+      if (!get_unit(a, rel / per, un)) continue;
+      const bool ends = a.reverse ? un.first : un.last;
+      if (a.states_only && ends) continue;  // nothing follows this window
+      h0 = rel % per * L::kHeads, chunks = (un.len + kC - 1) / kC;
+      if (!chunks) {  // no tokens: the last state is the first (and no unit is without blocks)
+        const int64_t size = (int64_t)a.NK * a.PV, from = ((int64_t)un.seq * a.H + h0) * size;
+        if (a.last)
+          for (int64_t i = t.lane; i < L::kHeads * size; i += 32) a.last[from + i] = a.start ? a.start[from + i] : 0.f;
+        continue;
+      }
+      if (!(ok = t.wait_free(kUnitFree + n % kUnitSlots, n / kUnitSlots))) break;
+      for (int i = t.lane; i < (int)(sizeof(LaPass) / 4); i += 32)
+        reinterpret_cast<uint32_t*>(&d->a)[i] = reinterpret_cast<const uint32_t*>(&a)[i];
+      if (t.lane == 0) {
+        d->un = un, d->u = rel / per, d->h0 = h0, d->planes = work.exact[pass] ? kPlanes : 1;
+        d->begins = a.reverse ? un.last : un.first, d->ends = ends;
+      }
+    } else if (!(ok = t.wait_free(kUnitFree + n % kUnitSlots, n / kUnitSlots))) {
+      break;
+    }
+    if (t.lane == 0) d->chunks = chunks;
+    t.arrive(kUnit + n % kUnitSlots);
+    ++n;
+    if (!left) break;
+    const LaPass& a = d->a;
+    const int8_t* map = work.map[pass];
+    const CUtensorMap *tq = &maps.m[map[0]], *tk = &maps.m[map[1]], *tv = &maps.m[map[2]];
+    const int qh = h0 / a.q_div, kh = h0 / a.k_div, vh = h0 / a.v_div;  // (two heads: v_div is 1)
+    const bool two = PAIR || a.PV > 64, q = !a.states_only;
+    const uint32_t bytes = ((q ? 2 : 1) * (NT / 64) + (two ? 2 : 1)) * kAtomBytes;
+    const bool reverse = a.reverse;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      if (!(ok = t.wait_free(kFree + s, use))) break;
+      if (t.lane == 0) {
+        uint64_t* bar = &t.bars[kFull + s];
+        uint8_t* to = t.smem + s * L::kStage;
+        const int tok = (int)un.t0 + (reverse ? chunks - 1 - c : c) * kC;
+        mbar_expect_tx(bar, bytes);
 #pragma unroll
-        for (int kk = 0; kk < NT / 16; ++kk)
-          umma_f16(t.tmem + kColS1, q + Issue::koff(kk), k + Issue::koff(kk), id_s1, kk > 0);
+        for (int i = 0; i < NT / 64; ++i) tma_load_3d(to + L::kK + i * kAtomBytes, tk, 64 * i, kh, tok, bar);
+        if (q) {
+#pragma unroll
+          for (int i = 0; i < NT / 64; ++i) tma_load_3d(to + L::kQ + i * kAtomBytes, tq, 64 * i, qh, tok, bar);
+        }
+        tma_load_3d(to + L::kV, tv, 0, vh, tok, bar);
+        if (two) tma_load_3d(to + L::kV + kAtomBytes, tv, PAIR ? 0 : 64, PAIR ? vh + 1 : vh, tok, bar);
       }
       __syncwarp();
-      if (!withhold) mma.commit(kS1Full);
       if (++s == L::kStages) s = 0, ++use;
     }
-    if (c + kAhead >= t.chunks) continue;
-    if (!(ok = t.wait_free(kFree + ls, luse))) break;
-    if (t.lane == 0) {
-      uint64_t* bar = &t.bars[kFull + ls];
-      uint8_t* to = t.smem + ls * L::kStage;
-      const int tok = (int)t.token(a, c + kAhead);
-      mbar_expect_tx(bar, bytes);
-#pragma unroll
-      for (int i = 0; i < NT / 64; ++i) tma_load_3d(to + L::kK + i * kAtomBytes, tk, 64 * i, kh, tok, bar);
-      if (!a.states_only) {
-#pragma unroll
-        for (int i = 0; i < NT / 64; ++i) tma_load_3d(to + L::kQ + i * kAtomBytes, tq, 64 * i, qh, tok, bar);
-      }
-      tma_load_3d(to + L::kV, tv, 0, vh, tok, bar);
-      if (v_atoms == 2) tma_load_3d(to + L::kV + kAtomBytes, tv, PAIR ? 0 : 64, PAIR ? vh + 1 : vh, tok, bar);
-    }
-    __syncwarp();
-    if (++ls == L::kStages) ls = 0, ++luse;
   }
-  mma.drain(kDrain);
   // after a failure: what was issued lands before the CTA ends
   if (!ok)
 #pragma unroll 1
     for (int d = 0; d < L::kStages; ++d) {
-      const int n = luse - (d >= ls);  // the last use of stage d that was loaded
+      const int n = use - (d >= s);  // the last use of stage d that was loaded
       if (n >= 0) wait_polls(smem_u32(&t.bars[kFull + d]), (uint32_t)n & 1u, kDrainPolls);
     }
 }
 
 // dS = (upd o value)^T key, plane by plane.
 template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void ds_role(const Cta& t, const LaPass& a) {
+__device__ __forceinline__ void ds_role(const Cta& t) {
   using L = TcSmem<NT, PAIR, PL>;
   const Issue mma(t);
   constexpr uint32_t id_ds = idesc_bf16(128, NT, 0, 1);
   bool ok = true;
-  int s = 0, use = 0;
+  int s = 0, use = 0, g = 0, m = 0;  // m: planes so far
+  Units at(t, L::kUnits);
 #pragma unroll 1
-  for (int c = 0; ok && c < t.chunks; ++c) {
-    if (!(ok = t.wait(kReady + s, use)) || !(ok = t.wait(kDsFree, c))) break;  // (the first time: S is loaded)
+  while (ok && at.next())
+#pragma unroll 1
+  for (int c = 0; c < at.d->chunks; ++c, ++g) {
+    if (!(ok = t.wait(kReady + s, use)) || !(ok = t.wait(kDsFree, g))) break;  // (the unit's first: S is loaded)
     const uint64_t k_mn = mma.at(mma.mn_major, s * L::kStage + L::kK);
 #pragma unroll 1
-    for (int p = 0; p < kPlanes; ++p) {
-      const int m = kPlanes * c + p, slot = m & 1;
+    for (int p = 0; p < kPlanes; ++p, ++m) {
+      const int slot = m & 1;
       if (!(ok = t.wait(kUvFull + slot, m >> 1))) break;
       tc_fence_after();
       if (mma.leader) {
@@ -335,30 +402,60 @@ __device__ __forceinline__ void ds_role(const Cta& t, const LaPass& a) {
     mma.commit(kFree + s);
     if (++s == L::kStages) s = 0, ++use;
   }
-  mma.drain(kDrain + 1);
+  mma.drain(kDrain);
 }
 
-// Yi^T = S query^T and Ya^T = value^T P^T.
+// S1 = query key^T, a block ahead; Yi^T = S query^T and Ya^T = value^T P^T.
 template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void y_role(const Cta& t, const LaPass& a) {
+__device__ __forceinline__ void y_role(const Cta& t, int withhold) {
   using L = TcSmem<NT, PAIR, PL>;
   const Issue mma(t);
-  constexpr uint32_t id_yi = idesc_bf16(128, kC, 0, 0), id_ya = idesc_bf16(128, PAIR ? 2 * kC : kC, 1, 0);
+  constexpr uint32_t id_s1 = idesc_bf16(64, kC, 0, 0), id_yi = idesc_bf16(128, kC, 0, 0),
+                     id_ya = idesc_bf16(128, PAIR ? 2 * kC : kC, 1, 0);
   constexpr int sp_slots = PAIR ? 1 : 2;
+  Units at(t, L::kUnits), ahead(t, L::kUnits);  // of Y, and of S1 (this one gives no slot back)
   bool ok = true;
-  int s = 0, use = 0;
+  int s = 0, use = 0, s1 = 0, s1use = 0, m = 0;  // stages of Y and of S1; m: planes of S so far
+  int left = 0, left1 = 0, planes = 1;           // blocks left of either's unit
 #pragma unroll 1
-  for (int c = 0; ok && c < t.chunks; ++c) {
-    if (!(ok = t.wait(kFull + s, use)) || !(ok = t.wait_free(kYFree, c))) break;
+  for (int g = -1;; ++g) {
+    while (left1 == 0) {
+      if (!(ok = ahead.peek())) break;
+      left1 = ahead.d->chunks;
+    }
+    if (!ok) break;
+    if (left1 > 0) {
+      --left1;
+      // the tiles as they landed: what a last block holds past its end is masked in P
+      if (!(ok = t.wait(kFull + s1, s1use)) || !(ok = t.wait_free(kS1Free, g + 1))) break;
+      tc_fence_after();
+      if (mma.leader) {
+        const uint64_t q = mma.at(mma.k_major, s1 * L::kStage + L::kQ), k = mma.at(mma.k_major, s1 * L::kStage + L::kK);
+#pragma unroll 1
+        for (int kk = 0; kk < NT / 16; ++kk)
+          umma_f16(t.tmem + kColS1, q + Issue::koff(kk), k + Issue::koff(kk), id_s1, kk > 0);
+      }
+      __syncwarp();
+      if (!withhold) mma.commit(kS1Full);
+      if (++s1 == L::kStages) s1 = 0, ++s1use;
+    }
+    if (g < 0) continue;
+    while (left == 0) {
+      if (!(ok = at.next())) break;
+      left = at.d->chunks, planes = PL > 1 ? at.d->planes : 1;
+    }
+    if (!ok) break;  // the end of the list, or a wait that gave up
+    --left;
+    if (!(ok = t.wait_free(kYFree, g))) break;
     const uint64_t q = mma.at(mma.k_major, s * L::kStage + L::kQ);
 #pragma unroll 1
-    for (int p = 0; p < PL; ++p) {
-      const int m = PL * c + p, slot = m % sp_slots;
+    for (int p = 0; p < planes; ++p, ++m) {
+      const int slot = m % sp_slots;
       if (!(ok = t.wait(kSpFull + slot, m / sp_slots))) break;
       tc_fence_after();
       if (mma.leader) {
         const uint32_t sp = t.tmem + (slot ? kColSp1 : kColSp0);
-#pragma unroll
+#pragma unroll 1
         for (int kk = 0; kk < NT / 16; ++kk)
           umma_f16_ta(t.tmem + kColYi, sp + kk * 8, q + Issue::koff(kk), id_yi, p > 0 || kk > 0);
       }
@@ -366,233 +463,247 @@ __device__ __forceinline__ void y_role(const Cta& t, const LaPass& a) {
       mma.commit(kSpFree + slot);
     }
     if (!ok) break;
-    if (!(ok = t.wait(kReady + s, use)) || !(ok = t.wait(kPFull + (c & 1), c >> 1))) break;
+    if (!(ok = t.wait(kReady + s, use)) || !(ok = t.wait(kPFull + (g & 1), g >> 1))) break;
     tc_fence_after();
     if (mma.leader) {
       const uint64_t v_mn = mma.at(mma.mn_major, s * L::kStage + L::kV);
 #pragma unroll 1
-      for (int p = 0; p < PL; ++p) {
-        const uint64_t pm = mma.at(mma.k_major, L::kP + ((c & 1) * L::kPTiles + p) * kAtomBytes);
-#pragma unroll
+      for (int p = 0; p < planes; ++p) {
+        const uint64_t pm = mma.at(mma.k_major, L::kP + ((g & 1) * L::kPTiles + p) * kAtomBytes);
+#pragma unroll 1
         for (int kk = 0; kk < kC / 16; ++kk)
           umma_f16(t.tmem + kColYa, v_mn + kk * 128, pm + kk * 2, id_ya, p > 0 || kk > 0);
       }
     }
     __syncwarp();
-    mma.commit(kPFree + (c & 1));
+    mma.commit(kPFree + (g & 1));
     mma.commit(kYFull);
     mma.commit(kFree + s);  // (S1 of this block was done before its P)
     if (++s == L::kStages) s = 0, ++use;
   }
-  mma.drain(kDrain + 2);
+  mma.drain(kDrain + 1);
 }
 
 // One head: lane l takes tokens 2 l, 2 l + 1 of each block.  Two: half a warp each, 4 tokens a lane.
 template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void gate_role(const Cta& t, const LaPass& a, int h0, int unit) {
+__device__ __forceinline__ void gate_role(const Cta& t) {
   using L = TcSmem<NT, PAIR, PL>;
   constexpr int kLanes = 32 / L::kHeads, kTok = kC / kLanes;
-  const int which = PAIR ? t.lane >> 4 : 0, l = t.lane & (kLanes - 1), i0 = kTok * l, h = h0 + which;
-  const float sr = a.reverse ? 1.f : a.scale, su = a.reverse ? a.scale : 1.f;
-  const float* from = a.log_decay + h;
-  double total = 0.0;
-  float x[kTok];
-  auto load = [&](int c) {
-    if (c >= t.chunks) return;
-    const int64_t tok = t.token(a, c) + i0;
-    const int left = t.rows(a, c) - i0;
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) x[j] = j < left ? from[a.per_token ? (tok + j) * a.H : 0] : 0.f;
-  };
-  load(0);
+  const int which = PAIR ? t.lane >> 4 : 0, l = t.lane & (kLanes - 1), i0 = kTok * l;
+  Units at(t, L::kUnits);
+  int g = 0;
 #pragma unroll 1
-  for (int c = 0; c < t.chunks; ++c) {
-    double sum[kTok];  // inclusive sums from the block's start
+  while (at.next()) {
+    const LaPass& a = at.d->a;
+    const bool reverse = a.reverse;
+    const float sr = reverse ? 1.f : a.scale, su = reverse ? a.scale : 1.f;
+    const float* from = a.log_decay + at.d->h0 + which;
+    const int64_t pitch = a.per_token ? a.H : 0;
+    double total = 0.0;
+    float x[kTok];
+    auto load = [&](int c) {
+      if (c >= at.d->chunks) return;
+      const int64_t tok = at.d->token(c) + i0;
+      const int left = at.d->rows(c) - i0;
 #pragma unroll
-    for (int j = 0; j < kTok; ++j) sum[j] = log2_clamped(x[j]) + (j ? sum[j - 1] : 0.0);
-    load(c + 1);
-    double before = sum[kTok - 1];
+      for (int j = 0; j < kTok; ++j) x[j] = j < left ? from[(tok + j) * pitch] : 0.f;
+    };
+    load(0);
+#pragma unroll 1
+    for (int c = 0; c < at.d->chunks; ++c, ++g) {
+      double sum[kTok];  // inclusive sums from the block's start
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, before, o, kLanes);
-      if (l >= o) before += v;
+      for (int j = 0; j < kTok; ++j) sum[j] = log2_clamped(x[j]) + (j ? sum[j - 1] : 0.0);
+      load(c + 1);
+      double before = sum[kTok - 1];
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, before, o, kLanes);
+        if (l >= o) before += v;
+      }
+      const double end = __shfl_sync(0xffffffffu, before, kLanes - 1, kLanes);
+      before -= sum[kTok - 1];
+      const int slot = g % kGateSlots;
+      if (!t.wait_free(kGFree + slot, g / kGateSlots)) return;
+      Gate* to = reinterpret_cast<Gate*>(t.smem + L::kGate) + slot * L::kHeads + which;
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        const double cc = before + sum[j];
+        float hi, lo;
+        const float from_start = exp2_split(cc, hi, lo);
+        to->chi[i0 + j] = hi, to->clo[i0 + j] = lo;
+        const float to_end = exp2_split(end - cc, hi, lo);
+        to->row[i0 + j] = (reverse ? to_end : from_start) * sr;
+        to->upd[i0 + j] = (reverse ? from_start : to_end) * su;
+      }
+      if (l == 0) {
+        float hi, lo;
+        to->decay = exp2_split(end, hi, lo);
+      }
+      total += end;
+      t.arrive(kGFull + slot);
     }
-    const double end = __shfl_sync(0xffffffffu, before, kLanes - 1, kLanes);
-    before -= sum[kTok - 1];
-    const int slot = c % kGateSlots;
-    if (!t.wait_free(kGFree + slot, c / kGateSlots)) return;
-    Gate* g = reinterpret_cast<Gate*>(t.smem + L::kGate) + slot * L::kHeads + which;
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-      const double cc = before + sum[j];
+    if (a.states_only && l == 0) {
       float hi, lo;
-      const float from_start = exp2_split(cc, hi, lo);
-      g->chi[i0 + j] = hi, g->clo[i0 + j] = lo;
-      const float to_end = exp2_split(end - cc, hi, lo);
-      g->row[i0 + j] = (a.reverse ? to_end : from_start) * sr;
-      g->upd[i0 + j] = (a.reverse ? from_start : to_end) * su;
+      a.window_decay[(int64_t)at.d->u * a.H + at.d->h0 + which] = exp2_split(total, hi, lo);
     }
-    if (l == 0) {
-      float hi, lo;
-      g->decay = exp2_split(end, hi, lo);
-    }
-    total += end;
-    t.arrive(kGFull + slot);
-  }
-  if (a.states_only && l == 0) {
-    float hi, lo;
-    a.window_decay[(int64_t)unit * a.H + h] = exp2_split(total, hi, lo);
   }
 }
 
 // S1 -> P.  Warp q holds rows 16 q .. 16 q + 15 of S1 (lanes 0 .. 15 of its quarter of tensor
 // memory: a product of 64 rows puts 16 in each quarter).
 template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void mask_role(const Cta& t, const LaPass& a) {
-  constexpr int planes = PL;
+__device__ __forceinline__ void mask_role(const Cta& t) {
   using L = TcSmem<NT, PAIR, PL>;
   const int q = threadIdx.x / 32 & 3;
   const int gr = t.lane >> 2, gc = (t.lane & 3) * 2;
   const int i0 = 16 * q + gr;
+  const uint32_t lanes = (uint32_t)(32 * q) << 16;
+  Units at(t, L::kUnits);
   uint8_t* P = t.smem + L::kP;
-  const int sign = a.reverse ? -1 : 1;
-  const float fsign = (float)sign;
   auto put = [&](uint8_t* tile, int i, int j, uint32_t v) {
     *reinterpret_cast<uint32_t*>(tile + sw128_off(i, j >> 3) + (j & 7) * 2) = v;
   };
-  if (!a.states_only) {  // the tiles above the diagonal stay zero
+  int g = 0;
 #pragma unroll 1
-    for (int n = 0; n < 8; ++n)
+  while (at.next()) {
+    const LaPass& a = at.d->a;
+    const bool reverse = a.reverse, states = a.states_only;
+    const float scale = a.scale, fsign = reverse ? -1.f : 1.f;
+    const int sign = reverse ? -1 : 1, planes = PL > 1 ? at.d->planes : 1;
+    // the pairs of column tiles with any j in reach; the others are zero (written anyway for the
+    // first two blocks of a unit: another unit's direction may have filled them)
+    const int b0 = reverse ? q : 0, b1 = reverse ? 4 : q + 1;
 #pragma unroll 1
-      for (int p = 0; p < 2 * L::kPTiles; ++p) {
-        put(P + p * kAtomBytes, i0, 8 * n + gc, 0u);
-        put(P + p * kAtomBytes, i0 + 8, 8 * n + gc, 0u);
-      }
-  }
+    for (int c = 0; c < at.d->chunks; ++c, ++g) {
+      const int slot = g % kGateSlots;
+      if (!t.wait(kGFull + slot, g / kGateSlots)) return;
+      if (!states) {
+        const Gate* gate = reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads;
+        if (!t.wait(kS1Full, g) || !t.wait_free(kPFree + (g & 1), g >> 1)) return;
+        tc_fence_after();
+        const int from = c < 2 ? 0 : b0, to = c < 2 ? 4 : b1;
 #pragma unroll 1
-  for (int c = 0; c < t.chunks; ++c) {
-    const int slot = c % kGateSlots;
-    if (!t.wait(kGFull + slot, c / kGateSlots)) return;
-    if (!a.states_only) {
-      const Gate* g = reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads;
-      if (!t.wait(kS1Full, c) || !t.wait_free(kPFree + (c & 1), c >> 1)) return;
-      tc_fence_after();
-      // the column tiles with any j in reach, two at a time
-      const int b0 = a.reverse ? q : 0, b1 = a.reverse ? 4 : q + 1;
-#pragma unroll 1
-      for (int b = b0; b < b1; ++b) {
-        uint32_t r[8];
-        tmem_ld_16x256_x2(t.tmem + ((uint32_t)(32 * q) << 16) + kColS1 + 16 * b, r);
-        tmem_ld_wait();
+        for (int b = from; b < to; ++b) {
+          uint32_t r[8];
+          tmem_ld_16x256_x2(t.tmem + lanes + kColS1 + 16 * b, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int hh = 0; hh < L::kHeads; ++hh) {
-          const float hi0 = g[hh].chi[i0], hi1 = g[hh].chi[i0 + 8], lo0 = g[hh].clo[i0], lo1 = g[hh].clo[i0 + 8];
+          for (int hh = 0; hh < L::kHeads; ++hh) {
+            const float hi0 = gate[hh].chi[i0], hi1 = gate[hh].chi[i0 + 8], lo0 = gate[hh].clo[i0], lo1 = gate[hh].clo[i0 + 8];
 #pragma unroll
-          for (int nn = 0; nn < 2; ++nn) {
-            const int j = 16 * b + 8 * nn + gc;
-            const float2 hj = *reinterpret_cast<const float2*>(&g[hh].chi[j]);
-            const float2 lj = *reinterpret_cast<const float2*>(&g[hh].clo[j]);
-            float v[4];
+            for (int nn = 0; nn < 2; ++nn) {
+              const int j = 16 * b + 8 * nn + gc;
+              const float2 hj = *reinterpret_cast<const float2*>(&gate[hh].chi[j]);
+              const float2 lj = *reinterpret_cast<const float2*>(&gate[hh].clo[j]);
+              float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float dh = (e >> 1 ? hi1 : hi0) - (e & 1 ? hj.y : hj.x);
-              const float dl = (e >> 1 ? lo1 : lo0) - (e & 1 ? lj.y : lj.x);
-              const int ahead = i0 + 8 * (e >> 1) - j - (e & 1);  // i - j
-              v[e] = sign * ahead >= 0 ? __uint_as_float(r[4 * nn + e]) * ex2(fsign * (dh + dl)) * a.scale : 0.f;
-            }
+              for (int e = 0; e < 4; ++e) {
+                const float dh = (e >> 1 ? hi1 : hi0) - (e & 1 ? hj.y : hj.x);
+                const float dl = (e >> 1 ? lo1 : lo0) - (e & 1 ? lj.y : lj.x);
+                const int ahead = i0 + 8 * (e >> 1) - j - (e & 1);  // i - j
+                v[e] = sign * ahead >= 0 ? __uint_as_float(r[4 * nn + e]) * ex2(fsign * (dh + dl)) * scale : 0.f;
+              }
 #pragma unroll
-            for (int p = 0; p < planes; ++p) {
-              const uint32_t x = bf16x2(v[0], v[1]), y = bf16x2(v[2], v[3]);
-              uint8_t* tile = P + ((c & 1) * L::kPTiles + (PAIR ? hh : p)) * kAtomBytes;
-              put(tile, i0, j, x);
-              put(tile, i0 + 8, j, y);
-              v[0] -= bf16_lo(x), v[1] -= bf16_hi(x), v[2] -= bf16_lo(y), v[3] -= bf16_hi(y);
+              for (int p = 0; p < PL; ++p) {
+                if (p >= planes) break;
+                const uint32_t x = bf16x2(v[0], v[1]), y = bf16x2(v[2], v[3]);
+                uint8_t* tile = P + ((g & 1) * L::kPTiles + (PAIR ? hh : p)) * kAtomBytes;
+                put(tile, i0, j, x);
+                put(tile, i0 + 8, j, y);
+                v[0] -= bf16_lo(x), v[1] -= bf16_hi(x), v[2] -= bf16_lo(y), v[3] -= bf16_hi(y);
+              }
             }
           }
         }
+        tc_fence_before();
+        t.arrive(kS1Free);
+        fence_proxy_async();
+        t.arrive(kPFull + (g & 1));
       }
-      tc_fence_before();
-      t.arrive(kS1Free);
-      fence_proxy_async();
-      t.arrive(kPFull + (c & 1));
+      t.arrive(kGFree + slot);
     }
-    t.arrive(kGFree + slot);
   }
 }
 
 // value -> the planes of upd o value in tensor memory, transposed on the way.  Warp w makes rows
 // 32 (w % 4) .. and half of the block's tokens.
 template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void decay_role(const Cta& t, const LaPass& a) {
+__device__ __forceinline__ void decay_role(const Cta& t) {
   using L = TcSmem<NT, PAIR, PL>;
   const int w = threadIdx.x / 32 - kDecayWarp, q = w & 3, half = w >> 2, lane = t.lane;
   const int head = PAIR ? q >> 1 : 0;
-  const bool active = (PAIR ? 32 * q & 63 : 32 * q) < a.PV;
-  int s = 0, use = 0;
+  const uint32_t uv = t.tmem + ((uint32_t)(32 * q) << 16) + kColUv + 16 * half;
+  Units at(t, L::kUnits);
+  int s = 0, use = 0, g = 0, m = 0;  // m: planes so far
 #pragma unroll 1
-  for (int c = 0; c < t.chunks; ++c) {
-    const int slot = c % kGateSlots, rows = t.rows(a, c);
-    uint8_t* tiles = t.smem + s * L::kStage;
-    if (!t.wait(kFull + s, use)) return;
-    if (rows < kC) {
-      // the sequence ends inside the block: what follows is another's, and 0 * NaN is NaN.  A
-      // row of key and value is 8 pieces of 16 bytes in each of up to 4 atoms
-      constexpr int kAtoms = NT / 64 + 2;
+  while (at.next()) {
+    const bool active = (PAIR ? 32 * q & 63 : 32 * q) < at.d->a.PV;
 #pragma unroll 1
-      for (int i = rows + w; i < kC; i += 8)
-        if (lane < 8 * kAtoms)
-          *reinterpret_cast<uint4*>(tiles + L::kK + (lane >> 3) * kAtomBytes + i * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async();
-    }
-    t.arrive(kReady + s);
-    if (rows < kC && !t.wait(kReady + s, use)) return;
-    if (++s == L::kStages) s = 0, ++use;
-    if (!t.wait(kGFull + slot, c / kGateSlots)) return;
-    const float* u = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads + head)->upd + 32 * half;
-    float x[2][8][2];  // [half of the rows][4 k step of 16 tokens + matrix][token of the pair]
-    if (active) {
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const int j = 32 * half + 16 * kk + (lane & 7) + ((lane >> 4) & 1) * 8;
-        const float2 ua = *reinterpret_cast<const float2*>(&u[16 * kk + 2 * (lane & 3)]);
-        const float2 ub = *reinterpret_cast<const float2*>(&u[16 * kk + 8 + 2 * (lane & 3)]);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int p = 32 * q + 16 * hf + ((lane >> 3) & 1) * 8;
-          uint32_t v[4];
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                       : "r"(smem_u32(tiles + L::kV + (p >> 6) * kAtomBytes + sw128_off(j, (p & 63) >> 3)))
-                       : "memory");
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            x[hf][4 * kk + m][0] = bf16_lo(v[m]) * (m < 2 ? ua.x : ub.x);
-            x[hf][4 * kk + m][1] = bf16_hi(v[m]) * (m < 2 ? ua.y : ub.y);
-          }
-        }
+    for (int c = 0; c < at.d->chunks; ++c, ++g) {
+      const int slot = g % kGateSlots, rows = at.d->rows(c);
+      uint8_t* tiles = t.smem + s * L::kStage;
+      if (!t.wait(kFull + s, use)) return;
+      if (rows < kC) {
+        // the sequence ends inside the block: what follows is another's, and 0 * NaN is NaN.  A
+        // row of key and value is 8 pieces of 16 bytes in each of up to 4 atoms
+        constexpr int kAtoms = NT / 64 + 2;
+#pragma unroll 1
+        for (int i = rows + w; i < kC; i += 8)
+          if (lane < 8 * kAtoms)
+            *reinterpret_cast<uint4*>(tiles + L::kK + (lane >> 3) * kAtomBytes + i * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
       }
-    }
-    t.arrive(kGFree + slot);
-#pragma unroll 1
-    for (int p = 0; p < kPlanes; ++p) {
-      const int m = kPlanes * c + p, us = m & 1;
-      if (!t.wait_free(kUvFree + us, m >> 1)) return;
-      tc_fence_after();
+      t.arrive(kReady + s);
+      if (rows < kC && !t.wait(kReady + s, use)) return;
+      if (++s == L::kStages) s = 0, ++use;
+      if (!t.wait(kGFull + slot, g / kGateSlots)) return;
+      const float* u = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + slot * L::kHeads + head)->upd + 32 * half;
+      float x[2][8][2];  // [half of the rows][4 k step of 16 tokens + matrix][token of the pair]
       if (active) {
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t v[8];
+        for (int kk = 0; kk < 2; ++kk) {
+          const int j = 32 * half + 16 * kk + (lane & 7) + ((lane >> 4) & 1) * 8;
+          const float2 ua = *reinterpret_cast<const float2*>(&u[16 * kk + 2 * (lane & 3)]);
+          const float2 ub = *reinterpret_cast<const float2*>(&u[16 * kk + 8 + 2 * (lane & 3)]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[i] = bf16x2(x[hf][i][0], x[hf][i][1]);
-            x[hf][i][0] -= bf16_lo(v[i]), x[hf][i][1] -= bf16_hi(v[i]);
+          for (int hf = 0; hf < 2; ++hf) {
+            const int p = 32 * q + 16 * hf + ((lane >> 3) & 1) * 8;
+            uint32_t v[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(smem_u32(tiles + L::kV + (p >> 6) * kAtomBytes + sw128_off(j, (p & 63) >> 3)))
+                         : "memory");
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[hf][4 * kk + k][0] = bf16_lo(v[k]) * (k < 2 ? ua.x : ub.x);
+              x[hf][4 * kk + k][1] = bf16_hi(v[k]) * (k < 2 ? ua.y : ub.y);
+            }
           }
-          tmem_st_16x128_x4(t.tmem + ((uint32_t)(32 * q + 16 * hf) << 16) + kColUv + 32 * us + 16 * half, v);
         }
-        tmem_st_wait();
       }
-      tc_fence_before();
-      t.arrive(kUvFull + us);
+      t.arrive(kGFree + slot);
+#pragma unroll 1
+      for (int p = 0; p < kPlanes; ++p, ++m) {
+        const int us = m & 1;
+        if (!t.wait_free(kUvFree + us, m >> 1)) return;
+        tc_fence_after();
+        if (active) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              v[i] = bf16x2(x[hf][i][0], x[hf][i][1]);
+              x[hf][i][0] -= bf16_lo(v[i]), x[hf][i][1] -= bf16_hi(v[i]);
+            }
+            tmem_st_16x128_x4(uv + ((uint32_t)(16 * hf) << 16) + 32 * us, v);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        t.arrive(kUvFull + us);
+      }
     }
   }
 }
@@ -664,141 +775,155 @@ __device__ __forceinline__ void put_state(uint32_t ds, const float (&S)[NC], con
   move_state<NC, true>(ds, at, lane, row0, n0, rows, cols);
 }
 
-// Plane p of the state that step c's outputs see, to tensor memory.
+// S in registers: warp w (of 8) holds rows 32 (w % 4) .. and half of the columns.  Step c = -1 of a
+// unit takes the start state the way the others take dS, from the same columns, so that there
+// is one piece of code for what follows either.
 template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ bool put_plane(const Cta& t, const float (&S)[NT / 2], bool active, uint32_t lanes, int half,
-                                          int c, int p) {
-  constexpr int NC = NT / 2, slots = PAIR ? 1 : 2;
-  const int m = PL * c + p, slot = m % slots;
-  if (!t.wait_free(kSpFree + slot, m / slots)) return false;
-  tc_fence_after();
-  if (active) {
-    const uint32_t to = t.tmem + lanes + (slot ? kColSp1 : kColSp0) + half * (NC / 2);
-#pragma unroll
-    for (int b = 0; b < NC / 32; ++b) {
-      uint32_t v[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x = S[32 * b + 2 * i], y = S[32 * b + 2 * i + 1];
-        v[i] = bf16x2(x, y);
-#pragma unroll
-        for (int k = 0; k < PL - 1; ++k) {
-          if (k >= p) break;
-          x -= bf16_lo(v[i]), y -= bf16_hi(v[i]);
-          v[i] = bf16x2(x, y);
-        }
-      }
-      tmem_st16(to + 16 * b, v);
-    }
-    tmem_st_wait();
-  }
-  tc_fence_before();
-  t.arrive(kSpFull + slot);
-  return true;
-}
-
-// S in registers: warp w (of 8) holds rows 32 (w % 4) .. and half of the columns.
-template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void state_role(const Cta& t, const LaPass& a, const Unit& un, int u, int h0) {
+__device__ __forceinline__ void state_role(const Cta& t) {
   using L = TcSmem<NT, PAIR, PL>;
   constexpr int NC = NT / 2, sp_slots = PAIR ? 1 : 2;  // columns of a thread
   const int w = threadIdx.x / 32 - kStateWarp, q = w & 3, half = w >> 2;
-  const int head = PAIR ? q >> 1 : 0, h = h0 + head;
+  const int head = PAIR ? q >> 1 : 0;
   const int row0 = PAIR ? 32 * q & 63 : 32 * q;  // the warp's first row of the head
-  const bool active = row0 < a.PV;
   const int n0 = half * NC;
-  const bool begins = a.reverse ? un.last : un.first, ends = a.reverse ? un.first : un.last;
   const uint32_t lanes = (uint32_t)(32 * q) << 16;
-  const int64_t state_at = ((int64_t)un.seq * a.H + h) * a.NK * a.PV;
   const uint32_t ds = t.tmem + lanes + kColDs + n0;  // the thread's part of dS
-  auto window_at = [&](float* base, int64_t win) {
-    return StateAt{base + (win * a.H + h) * a.PV * a.NK, (int64_t)a.NK, 1};
-  };
+  Units at(t, L::kUnits);
   float S[NC];
-  {
-    StateAt from{nullptr, a.NK, 1};
-    if (!begins && !a.states_only)
-      from = window_at(a.carry, u);
-    else if (begins && a.start)
-      from = StateAt{const_cast<float*>(a.start) + state_at, a.sr, a.sc};
-    move_state<NC, false>(ds, from, t.lane, row0, n0, from.base ? a.PV : 0, a.NK);
-#pragma unroll
-    for (int b = 0; b < NC / 16; ++b) {
-      uint32_t v[16];
-      tmem_ld16(ds + 16 * b, v);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[16 * b + i] = __uint_as_float(v[i]);
-    }
-  }
-  // windows whose state is wanted: forward, after the window's last block; reverse, before it
-  auto wanted = [&](int ci) { return a.dump && (ci == t.chunks - 1 || (ci + 1) * kC % a.window == 0); };
-  auto dump_at = [&](int ci) { return window_at(a.dump, un.first_window + ci * kC / a.window); };
-  if (a.reverse && t.chunks && wanted(t.chunks - 1)) put_state<NC>(ds, S, dump_at(t.chunks - 1), t.lane, row0, n0, a.PV, a.NK);
-  tc_fence_before();
-  t.arrive(kDsFree);
-  if (!a.states_only && t.chunks)
-#pragma unroll
-    for (int p = 0; p < PL; ++p)
-      if (!put_plane<NT, PAIR, PL>(t, S, active, lanes, half, 0, p)) return;
+  int g = 0, m = 0;  // blocks and planes so far
 #pragma unroll 1
-  for (int c = 0; c < t.chunks; ++c) {
-    const int ci = a.reverse ? t.chunks - 1 - c : c;
-    if (!t.wait(kGFull + c % kGateSlots, c / kGateSlots)) return;
-    const float dec = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (c % kGateSlots) * L::kHeads + head)->decay;
-    const bool more = !a.states_only && c + 1 < t.chunks;
-    const int m = PL * (c + 1), slot = m % sp_slots;  // the next step's first plane goes out as S is made
-    if (!t.wait(kDsFull, c) || (more && !t.wait_free(kSpFree + slot, m / sp_slots))) return;
-    tc_fence_after();
-    const uint32_t sp = t.tmem + lanes + (slot ? kColSp1 : kColSp0) + half * (NC / 2);
+  while (at.next()) {
+    const LaPass& a = at.d->a;
+    const int h = at.d->h0 + head, planes = PL > 1 ? at.d->planes : 1;
+    const bool states = a.states_only;
+    const int64_t state_at = ((int64_t)at.d->un.seq * a.H + h) * a.NK * a.PV;
+    auto window_at = [&](float* base, int64_t win) {
+      return StateAt{base + (win * a.H + h) * a.PV * a.NK, (int64_t)a.NK, 1};
+    };
+    {
+      StateAt from{nullptr, a.NK, 1};
+      if (!at.d->begins) {
+        if (!states) from = window_at(a.carry, at.d->u);
+      } else if (a.start) {
+        from = StateAt{const_cast<float*>(a.start) + state_at, a.sr, a.sc};
+      }
+      move_state<NC, false>(ds, from, t.lane, row0, n0, from.base ? a.PV : 0, a.NK);
 #pragma unroll
-    for (int b = 0; b < NC / 16; ++b) {
-      uint32_t d[16], v[8];
-      tmem_ld16(ds + 16 * b, d);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(S[16 * b + i], dec, __uint_as_float(d[i]));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = bf16x2(S[16 * b + 2 * i], S[16 * b + 2 * i + 1]);
-      if (more) tmem_st8(sp + 8 * b, v);
+      for (int n = 0; n < NC; ++n) S[n] = 0.f;
     }
-    const int at = a.reverse ? ci - 1 : ci;  // the block whose window's state this may be
-    if (at >= 0 && wanted(at)) put_state<NC>(ds, S, dump_at(at), t.lane, row0, n0, a.PV, a.NK);
-    tc_fence_before();
-    t.arrive(kDsFree);
-    t.arrive(kGFree + c % kGateSlots);
-    if (more) {
-      tmem_st_wait();
-      tc_fence_before();
-      t.arrive(kSpFull + slot);
+#pragma unroll 1
+    for (int c = -1; c < at.d->chunks; ++c) {
+      float dec = 0.f;
+      if (c >= 0) {
+        if (!t.wait(kGFull + g % kGateSlots, g / kGateSlots)) return;
+        dec = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (g % kGateSlots) * L::kHeads + head)->decay;
+        if (!t.wait(kDsFull, g)) return;
+      }
+      const bool more = c + 1 < at.d->chunks, out = more && !states;
+      const int slot = m % sp_slots;  // the next step's first plane goes out as S is made
+      if (out && !t.wait_free(kSpFree + slot, m / sp_slots)) return;
+      tc_fence_after();
+      const uint32_t sp = t.tmem + lanes + (slot ? kColSp1 : kColSp0) + half * (NC / 2);
 #pragma unroll
-      for (int p = 1; p < PL; ++p)
-        if (!put_plane<NT, PAIR, PL>(t, S, active, lanes, half, c + 1, p)) return;
+      for (int b = 0; b < NC / 16; ++b) {
+        uint32_t d[16], v[8];
+        tmem_ld16(ds + 16 * b, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(S[16 * b + i], dec, __uint_as_float(d[i]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = bf16x2(S[16 * b + 2 * i], S[16 * b + 2 * i + 1]);
+        if (out) tmem_st8(sp + 8 * b, v);
+      }
+      if (out) tmem_st_wait();
+      // Copies that are wanted: of the windows' states (forward, after a window's last block;
+      // reverse, before it), and of the unit's last one.
+      const int bl = a.reverse ? at.d->chunks - 2 - c : c;
+      const bool dump = a.dump && bl >= 0 && (bl == at.d->chunks - 1 || (bl + 1) * kC % a.window == 0);
+      const bool last = !more && (states || (a.last && at.d->ends));
+      if (dump || last) {
+#pragma unroll
+        for (int b = 0; b < NC / 16; ++b) {
+          uint32_t v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(S[16 * b + i]);
+          tmem_st16(ds + 16 * b, v);
+        }
+        tmem_st_wait();
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          if (!(k ? last : dump)) continue;
+          StateAt to = window_at(k ? a.carry : a.dump, k ? at.d->u : at.d->un.first_window + bl * kC / a.window);
+          if (k && !states) to = StateAt{a.last + state_at, a.sr, a.sc};
+          move_state<NC, true>(ds, to, t.lane, row0, n0, a.PV, a.NK);
+        }
+      }
+      tc_fence_before();
+      if (out) {
+        t.arrive(kSpFull + slot);
+        ++m;
+      }
+      if (more) t.arrive(kDsFree);
+      if (c >= 0) {
+        t.arrive(kGFree + g % kGateSlots);
+        ++g;
+      }
+      if (PL > 1 && out) {  // the planes of what the first one leaves
+#pragma unroll 1
+        for (int p = 1; p < planes; ++p, ++m) {
+          const int sl = m % sp_slots;
+          if (!t.wait_free(kSpFree + sl, m / sp_slots)) return;
+          tc_fence_after();
+          const uint32_t to = t.tmem + lanes + (sl ? kColSp1 : kColSp0) + half * (NC / 2);
+#pragma unroll
+          for (int b = 0; b < NC / 16; ++b) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              // made anew for each plane: kept across them, the remainders would not fit the registers
+              asm volatile("" : "+f"(S[16 * b + 2 * i]), "+f"(S[16 * b + 2 * i + 1]));
+              float x = S[16 * b + 2 * i], y = S[16 * b + 2 * i + 1];
+              v[i] = bf16x2(x, y);
+              x -= bf16_lo(v[i]), y -= bf16_hi(v[i]);
+              v[i] = bf16x2(x, y);
+              if (p > 1) v[i] = bf16x2(x - bf16_lo(v[i]), y - bf16_hi(v[i]));
+            }
+            tmem_st8(to + 8 * b, v);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          t.arrive(kSpFull + sl);
+        }
+      }
     }
   }
-  if (a.states_only)
-    put_state<NC>(ds, S, window_at(a.carry, u), t.lane, row0, n0, a.PV, a.NK);
-  else if (a.last && ends)
-    put_state<NC>(ds, S, StateAt{a.last + state_at, a.sr, a.sc}, t.lane, row0, n0, a.PV, a.NK);
 }
 
 // Yi, Ya -> out: warp q writes rows 32 q .., 16 tokens at a time.  Tensor memory is read in the layout of mma.sync's accumulators (registers are pairs of
 // tokens of one row), turned by transposing stores to shared memory, and written from there
 // in 16-byte pieces (single 2-byte stores took 16 cycles each, 5 of a block's 9 thousand).
 template <int NT, bool PAIR, int PL>
-__device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) {
+__device__ __forceinline__ void out_role(const Cta& t) {
   using L = TcSmem<NT, PAIR, PL>;
   const int q = threadIdx.x / 32 & 3;
-  const int head = PAIR ? q >> 1 : 0, h = h0 + head;
+  const int head = PAIR ? q >> 1 : 0;
   const int row0 = PAIR ? 32 * q & 63 : 32 * q;  // the warp's first row of the head
-  const bool active = row0 < a.PV;
   const uint32_t lanes = (uint32_t)(32 * q) << 16;
   uint8_t* stage = t.smem + L::kOut + q * kOutBytes;
   uint8_t* dots_in = t.smem + L::kDot + q * kDotBytes;
+  const int gr = t.lane >> 2, gc = (t.lane & 3) * 2;
+  Units walk(t, L::kUnits);
+  int g = 0;
+#pragma unroll 1
+  while (walk.next()) {
+  const LaPass& a = walk.d->a;
+  const int h = walk.d->h0 + head;
+  const bool active = row0 < a.PV;
+  const bool dots = PL > 1 && a.dot != nullptr;
   // The rows that step c's outputs are multiplied with, on their way while its products run.
   auto fetch_dots = [&](int c) {
-    const int64_t tok = t.token(a, c);
-    const int rows = t.rows(a, c);
+    const int64_t tok = walk.d->token(c);
+    const int rows = walk.d->rows(c);
     const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.dot) + (tok * a.dot_heads + h / a.dot_div) * a.PV + row0;
 #pragma unroll 1
     for (int k = 0; k < 8; ++k) {
@@ -812,16 +937,15 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
     cp_async_commit();
   };
 #pragma unroll 1
-  for (int c = 0; c < t.chunks; ++c) {
-    if constexpr (PL > 1) fetch_dots(c);
-    const float* rowf = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (c % kGateSlots) * L::kHeads + head)->row;
-    if (!t.wait(kGFull + c % kGateSlots, c / kGateSlots) || !t.wait(kYFull, c)) return;
+  for (int c = 0; c < walk.d->chunks; ++c, ++g) {
+    if (dots) fetch_dots(c);
+    const float* rowf = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (g % kGateSlots) * L::kHeads + head)->row;
+    if (!t.wait(kGFull + g % kGateSlots, g / kGateSlots) || !t.wait(kYFull, g)) return;
     tc_fence_after();
-    const int64_t tok = t.token(a, c);
-    const int rows = t.rows(a, c);
+    const int64_t tok = walk.d->token(c);
+    const int rows = walk.d->rows(c);
     const int64_t pitch = (int64_t)a.H * a.PV, at = tok * pitch + (int64_t)h * a.PV + row0;
-    const int gr = t.lane >> 2, gc = (t.lane & 3) * 2;
-    if constexpr (PL > 1) {
+    if (dots) {
       cp_async_wait_all();
       __syncwarp();
     }
@@ -852,7 +976,7 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
         for (int e = 0; e < 8; ++e)
           o[hf][e] = fmaf(__uint_as_float(yi[hf][e]), e < 4 ? (e & 1 ? f0.y : f0.x) : (e & 1 ? f1.y : f1.x),
                           __uint_as_float(ya[hf][e]));
-      if (!a.out_f32) {
+      if (PL == 1 || !a.out_f32) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const uint8_t* to = stage + (16 * b + 8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf + 16 * ((t.lane >> 3) & 1);
@@ -878,8 +1002,7 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
         }
         __syncwarp();
       }
-      if constexpr (PL > 1)
-        if (active) {  // sums over the warp's rows of out * dot, for the decay's gradient
+      if (dots && active) {  // sums over the warp's rows of out * dot, for the decay's gradient
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -907,8 +1030,8 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
           a.dots[((int64_t)q * a.tokens + tok + i) * a.H + h] = m == 0 ? sum[0] : m == 1 ? sum[1] : m == 2 ? sum[2] : sum[3];
       }
     }
-    t.arrive(kGFree + c % kGateSlots);
-    if (!active || a.out_f32) continue;
+    t.arrive(kGFree + g % kGateSlots);
+    if (!active || (PL > 1 && a.out_f32)) continue;
     __syncwarp();
     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at;
 #pragma unroll 4
@@ -919,51 +1042,43 @@ __device__ __forceinline__ void out_role(const Cta& t, const LaPass& a, int h0) 
     }
     __syncwarp();
   }
+  }
 }
 
-// Grid: units x heads (or pairs of heads), heads fastest.
+// Grid: a CTA per SM at most; CTA b takes units b, b + grid, ... of the list (units of a pass times
+// heads or pairs of heads, heads fastest).
 template <int NT, bool PAIR, int PL>
 __global__ void __launch_bounds__(kThreadsTc, 1)
-    la_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ LaPass a, unsigned int* status, uint32_t polls, int withhold) {
+    la_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcWork work, unsigned int* status,
+                 uint32_t polls, int withhold) {
   using L = TcSmem<NT, PAIR, PL>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
-  const int lanes_of_heads = PAIR ? a.H / 2 : a.H;
-  const int u = blockIdx.x / lanes_of_heads, h0 = (blockIdx.x % lanes_of_heads) * L::kHeads;
-  Unit un;
-  if (!get_unit(a, u, un)) return;
-  if (a.states_only && (a.reverse ? un.first : un.last)) return;  // nothing follows this window
   const int warp = threadIdx.x >> 5;
+  const bool states = work.pass[0].states_only;
   Cta t;
   t.smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset, so that accesses stay known as shared)
   t.bars = reinterpret_cast<uint64_t*>(t.smem + L::kBar);
   t.abort_flag = reinterpret_cast<volatile int*>(t.smem + L::kFlag);
   t.polls = polls;
   t.lane = threadIdx.x & 31;
-  t.t0 = un.t0, t.len = un.len;
-  t.chunks = (un.len + kC - 1) / kC;
   if (warp == 0) {
     tmem_alloc(&s_tmem, kTmem);
     tmem_relinquish();
   }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kBars; ++i) {
-      int n = 1;
-      if (i == kS1Free || (i >= kPFull && i < kPFree)) n = 4;
-      if ((i >= kReady && i < kFree) || (i >= kUvFull && i < kUvFree)) n = 8;
-      if (i == kYFree) n = 4;
-      if (i == kDsFree || (i >= kSpFull && i < kSpFree)) n = 8;
-      if (i >= kFree && i < kS1Full) n = a.states_only ? 1 : 2;
-      if (i >= kGFree && i < kDrain) n = a.states_only ? 20 : 24;
-      mbar_init(&t.bars[i], n);
-    }
-    *t.abort_flag = 0;
+  if (threadIdx.x >= 32 && threadIdx.x < 32 + kBars) {
+    const int i = threadIdx.x - 32;
+    int n = 1;
+    if (i == kS1Free || (i >= kPFull && i < kPFree) || i == kYFree) n = 4;
+    if ((i >= kReady && i < kFree) || (i >= kUvFull && i < kUvFree)) n = 8;
+    if (i == kDsFree || (i >= kSpFull && i < kSpFree)) n = 8;
+    if (i >= kFree && i < kS1Full) n = states ? 1 : 2;
+    if (i >= kGFree && i < kUnit) n = states ? 20 : 24;
+    if (i >= kUnitFree && i < kDrain) n = states ? 22 : 27;  // every warp but the load warp
+    mbar_init(&t.bars[i], n);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    prefetch_tensormap(&tq);
-    prefetch_tensormap(&tk);
-    prefetch_tensormap(&tv);
   }
+  if (threadIdx.x == 0) *t.abort_flag = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -973,26 +1088,26 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   // 128 x (40 + 56 + 2 x 56 + 2 x 112 + 72) = 64512, are what the launch holds.
   if (warp < kMaskWarp) {
     set_regs_dec<40>();
-    if (warp == kLoadWarp)
-      load_role<NT, PAIR, PL>(t, a, &tq, &tk, &tv, h0, withhold);
-    else if (warp == kDsWarp)
-      ds_role<NT, PAIR, PL>(t, a);
-    else if (warp == kGateWarp)
-      gate_role<NT, PAIR, PL>(t, a, h0, u);
-    else if (warp == kYWarp && !a.states_only)
-      y_role<NT, PAIR, PL>(t, a);
+    if (warp == kLoadWarp) {
+      load_role<NT, PAIR, PL>(t, work, maps);
+    } else if (warp == kGateWarp) {
+      gate_role<NT, PAIR, PL>(t);
+    } else if (warp == kDsWarp) {
+      ds_role<NT, PAIR, PL>(t);
+    } else if (!states) {
+      y_role<NT, PAIR, PL>(t, withhold);
+    }
   } else if (warp < kDecayWarp) {
     set_regs_dec<56>();
-    mask_role<NT, PAIR, PL>(t, a);
+    mask_role<NT, PAIR, PL>(t);
   } else if (warp < kStateWarp) {
     set_regs_dec<56>();
-    decay_role<NT, PAIR, PL>(t, a);
+    decay_role<NT, PAIR, PL>(t);
   } else if (warp < kOutWarp) {
     set_regs_inc<112>();
-    state_role<NT, PAIR, PL>(t, a, un, u, h0);
-  } else {
-    set_regs_inc<72>();
-    if (!a.states_only) out_role<NT, PAIR, PL>(t, a, h0);
+    state_role<NT, PAIR, PL>(t);
+  } else if (!states) {
+    out_role<NT, PAIR, PL>(t);
   }
 
   __syncwarp();
@@ -1019,21 +1134,17 @@ bool make_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t toke
 }
 
 template <int NT, bool PAIR, int PL>
-cudaError_t launch_one(const LaPass& p, cudaStream_t st) {
+cudaError_t launch_one(const TcMaps& maps, const TcWork& work, cudaStream_t st) {
   auto* fn = la_tc_kernel<NT, PAIR, PL>;
   using L = TcSmem<NT, PAIR, PL>;
   static_assert(L::kBytes <= 227 * 1024, "tiles must fit the SM's shared memory");
-  CUtensorMap tq, tk, tv;
-  if (!make_map(&tq, p.query, p.NK, p.q_heads, p.tokens) || !make_map(&tk, p.key, p.NK, p.k_heads, p.tokens) ||
-      !make_map(&tv, p.value, p.PV, p.v_heads, p.tokens))
-    return cudaErrorInvalidValue;
+  static_assert(kBars + 32 <= kThreadsTc, "a thread per barrier");
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   // a poll takes 1 us (2000 cycles) at most: the bound in polls is within that of the wait limit
   const uint32_t polls = (uint32_t)std::min<long long>(std::max<long long>(device_wait_limit() / 2000, 1), 1u << 22);
-  const int64_t units = p.segmented ? p.max_windows : p.nseq;
-  fn<<<(unsigned)(units * (PAIR ? p.H / 2 : p.H)), kThreadsTc, L::kBytes, st>>>(
-      tq, tk, tv, p, device_status_word(), polls, device_withhold() & 4);
+  fn<<<(unsigned)std::min(work.total, device_sm_count()), kThreadsTc, L::kBytes, st>>>(
+      maps, work, device_status_word(), polls, device_withhold() & 4);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -1046,11 +1157,45 @@ bool la_tc_pairs(const LaPass& p) {
   return p.PV <= 64 && p.H % 2 == 0 && p.q_div % 2 == 0 && p.k_div % 2 == 0 && p.v_div == 1;
 }
 
-cudaError_t launch_la_tc(const LaPass& p, bool exact, cudaStream_t st) {
-  const bool narrow = p.NK <= 64;
-  if (exact) return narrow ? launch_one<64, false, kPlanes>(p, st) : launch_one<128, false, kPlanes>(p, st);
-  if (la_tc_pairs(p)) return narrow ? launch_one<64, true, 1>(p, st) : launch_one<128, true, 1>(p, st);
-  return narrow ? launch_one<64, false, 1>(p, st) : launch_one<128, false, 1>(p, st);
+cudaError_t launch_la_tc(const LaPass* p, int passes, cudaStream_t st) {
+  bool exact = false, pair = passes == 1 && la_tc_pairs(p[0]), narrow = true;
+  for (int i = 0; i < passes; ++i) {
+    exact |= p[i].dots != nullptr || p[i].out_f32;  // (only that instance writes fp32)
+    narrow &= p[i].NK <= 64;
+  }
+  pair &= !exact;
+  TcWork work{};
+  TcMaps maps;
+  const void* bases[4] = {};  // an operand that passes share has one map
+  int dims[4] = {}, counts[4] = {}, made = 0;
+  work.passes = passes;
+  int64_t total = 0;
+  for (int i = 0; i < passes; ++i) {
+    work.pass[i] = p[i];
+    work.exact[i] = p[i].dots != nullptr;
+    work.first[i] = (int)total;
+    const int64_t units = p[i].segmented ? p[i].max_windows : p[i].nseq;
+    total += units * (pair ? p[i].H / 2 : p[i].H);
+    const void* operand[3] = {p[i].query, p[i].key, p[i].value};
+    const int dim[3] = {p[i].NK, p[i].NK, p[i].PV}, heads[3] = {p[i].q_heads, p[i].k_heads, p[i].v_heads};
+    for (int o = 0; o < 3; ++o) {
+      int k = 0;
+      while (k < made && (bases[k] != operand[o] || dims[k] != dim[o] || counts[k] != heads[o])) ++k;
+      if (k == made) {
+        if (made == 4 || (operand[o] && !make_map(&maps.m[k], operand[o], dim[o], heads[o], p[i].tokens)))
+          return cudaErrorInvalidValue;
+        bases[made] = operand[o], dims[made] = dim[o], counts[made] = heads[o];
+        ++made;
+      }
+      work.map[i][o] = (int8_t)k;
+    }
+  }
+  if (total > (1ll << 31) - 1) return cudaErrorInvalidConfiguration;
+  if (total == 0) return cudaSuccess;
+  work.total = (int)total;
+  if (exact) return narrow ? launch_one<64, false, kPlanes>(maps, work, st) : launch_one<128, false, kPlanes>(maps, work, st);
+  if (pair) return narrow ? launch_one<64, true, 1>(maps, work, st) : launch_one<128, true, 1>(maps, work, st);
+  return narrow ? launch_one<64, false, 1>(maps, work, st) : launch_one<128, false, 1>(maps, work, st);
 }
 
 }  // namespace ssd
