@@ -99,7 +99,7 @@ struct Gate {
 
 // An output warp's own staging: 64 tokens x 32 rows of bf16 at 80 bytes a token, or 16 tokens of
 // fp32 at 144 (neither pitch has bank conflicts); and as much for the rows of the dot products.
-constexpr int kOutPitch = 80, kOutPitch32 = 144, kOutBytes = kC * kOutPitch, kDotBytes = kC * kOutPitch;
+constexpr int kOutPitch = 80, kOutPitch32 = 144, kOutBytes = kC * kOutPitch, kDotBytes = kC * kOutPitch, kSumBytes = 4 * 32 * 16;
 
 template <int NT, bool PAIR, int PL>
 struct TcSmem {
@@ -111,7 +111,8 @@ struct TcSmem {
   static constexpr int kGate = kP + 2 * kPTiles * kAtomBytes;
   static constexpr int kOut = kGate + (int)sizeof(Gate) * kHeads * kGateSlots;  // out warps: staged outputs, ...
   static constexpr int kDot = kOut + 4 * kOutBytes;                              // ... rows to multiply them with
-  static constexpr int kBar = kDot + 4 * kDotBytes;
+  static constexpr int kSum = kDot + (PL > 1 ? 4 * kDotBytes : 0);               // ... and the products' parts
+  static constexpr int kBar = kSum + (PL > 1 ? 4 * kSumBytes : 0);
   static constexpr int kFlag = kBar + 8 * kBars;
   static constexpr int kUnits = (kFlag + 4 + 15) / 16 * 16;
   static constexpr int kBytes = kUnits + kUnitSlots * (int)sizeof(UnitDesc) + 1024;                  // 1024: alignment of the base
@@ -161,6 +162,14 @@ __device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t t, uint32_t (&r)[8]) 
 __device__ __forceinline__ void tmem_st_16x128_x4(uint32_t t, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Waits for the loads so far, and ties the wait to the registers they fill.
+__device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
                : "memory");
 }
 
@@ -448,6 +457,7 @@ __device__ __forceinline__ void y_role(const Cta& t, int withhold) {
     --left;
     if (!(ok = t.wait_free(kYFree, g))) break;
     const uint64_t q = mma.at(mma.k_major, s * L::kStage + L::kQ);
+    // Ya goes between the planes of S: the third plane's slot is free once the first is done
 #pragma unroll 1
     for (int p = 0; p < planes; ++p, ++m) {
       const int slot = m % sp_slots;
@@ -461,22 +471,23 @@ __device__ __forceinline__ void y_role(const Cta& t, int withhold) {
       }
       __syncwarp();
       mma.commit(kSpFree + slot);
+      if (p) continue;
+      if (!(ok = t.wait(kReady + s, use)) || !(ok = t.wait(kPFull + (g & 1), g >> 1))) break;
+      tc_fence_after();
+      if (mma.leader) {
+        const uint64_t v_mn = mma.at(mma.mn_major, s * L::kStage + L::kV);
+#pragma unroll 1
+        for (int k = 0; k < planes; ++k) {
+          const uint64_t pm = mma.at(mma.k_major, L::kP + ((g & 1) * L::kPTiles + k) * kAtomBytes);
+#pragma unroll 1
+          for (int kk = 0; kk < kC / 16; ++kk)
+            umma_f16(t.tmem + kColYa, v_mn + kk * 128, pm + kk * 2, id_ya, k > 0 || kk > 0);
+        }
+      }
+      __syncwarp();
+      mma.commit(kPFree + (g & 1));
     }
     if (!ok) break;
-    if (!(ok = t.wait(kReady + s, use)) || !(ok = t.wait(kPFull + (g & 1), g >> 1))) break;
-    tc_fence_after();
-    if (mma.leader) {
-      const uint64_t v_mn = mma.at(mma.mn_major, s * L::kStage + L::kV);
-#pragma unroll 1
-      for (int p = 0; p < planes; ++p) {
-        const uint64_t pm = mma.at(mma.k_major, L::kP + ((g & 1) * L::kPTiles + p) * kAtomBytes);
-#pragma unroll 1
-        for (int kk = 0; kk < kC / 16; ++kk)
-          umma_f16(t.tmem + kColYa, v_mn + kk * 128, pm + kk * 2, id_ya, p > 0 || kk > 0);
-      }
-    }
-    __syncwarp();
-    mma.commit(kPFree + (g & 1));
     mma.commit(kYFull);
     mma.commit(kFree + s);  // (S1 of this block was done before its P)
     if (++s == L::kStages) s = 0, ++use;
@@ -531,7 +542,11 @@ __device__ __forceinline__ void gate_role(const Cta& t) {
         const double cc = before + sum[j];
         float hi, lo;
         const float from_start = exp2_split(cc, hi, lo);
-        to->chi[i0 + j] = hi, to->clo[i0 + j] = lo;
+        // signed, so that the decay between i and j is 2^(c_i - c_j) either way.  In one number
+        // where P is rounded to bf16: its error, 2^-24 of at most 9600, is a tenth of P's
+        const float sign = reverse ? -1.f : 1.f;
+        to->chi[i0 + j] = sign * (PL > 1 ? hi : hi + lo);
+        if (PL > 1) to->clo[i0 + j] = sign * lo;
         const float to_end = exp2_split(end - cc, hi, lo);
         to->row[i0 + j] = (reverse ? to_end : from_start) * sr;
         to->upd[i0 + j] = (reverse ? from_start : to_end) * su;
@@ -569,11 +584,13 @@ __device__ __forceinline__ void mask_role(const Cta& t) {
   while (at.next()) {
     const LaPass& a = at.d->a;
     const bool reverse = a.reverse, states = a.states_only;
-    const float scale = a.scale, fsign = reverse ? -1.f : 1.f;
-    const int sign = reverse ? -1 : 1, planes = PL > 1 ? at.d->planes : 1;
+    const float scale = a.scale;
+    const int planes = PL > 1 ? at.d->planes : 1;
     // the pairs of column tiles with any j in reach; the others are zero (written anyway for the
     // first two blocks of a unit: another unit's direction may have filled them)
     const int b0 = reverse ? q : 0, b1 = reverse ? 4 : q + 1;
+    // j <= i (reverse: j >= i) is sign * (i - j) >= 0, for the thread's rows i0, i0 + 8 and columns j, j + 1
+    const int sign = reverse ? -1 : 1;
 #pragma unroll 1
     for (int c = 0; c < at.d->chunks; ++c, ++g) {
       const int slot = g % kGateSlots;
@@ -583,41 +600,52 @@ __device__ __forceinline__ void mask_role(const Cta& t) {
         if (!t.wait(kS1Full, g) || !t.wait_free(kPFree + (g & 1), g >> 1)) return;
         tc_fence_after();
         const int from = c < 2 ? 0 : b0, to = c < 2 ? 4 : b1;
+        uint8_t* tiles = P + (g & 1) * L::kPTiles * kAtomBytes;
+        // the next columns are on their way while these are worked on; S1 is free before the last
+        uint32_t r[8], next[8];
+        tmem_ld_16x256_x2(t.tmem + lanes + kColS1 + 16 * from, r);
+        tmem_ld_wait8(r);
 #pragma unroll 1
         for (int b = from; b < to; ++b) {
-          uint32_t r[8];
-          tmem_ld_16x256_x2(t.tmem + lanes + kColS1 + 16 * b, r);
-          tmem_ld_wait();
+          if (b + 1 < to) tmem_ld_16x256_x2(t.tmem + lanes + kColS1 + 16 * (b + 1), next);
+          if (b + 1 == to) {
+            tc_fence_before();
+            t.arrive(kS1Free);
+          }
 #pragma unroll
           for (int hh = 0; hh < L::kHeads; ++hh) {
-            const float hi0 = gate[hh].chi[i0], hi1 = gate[hh].chi[i0 + 8], lo0 = gate[hh].clo[i0], lo1 = gate[hh].clo[i0 + 8];
+            const float hi0 = gate[hh].chi[i0], hi1 = gate[hh].chi[i0 + 8];
+            const float lo0 = PL > 1 ? gate[hh].clo[i0] : 0.f, lo1 = PL > 1 ? gate[hh].clo[i0 + 8] : 0.f;
 #pragma unroll
             for (int nn = 0; nn < 2; ++nn) {
               const int j = 16 * b + 8 * nn + gc;
               const float2 hj = *reinterpret_cast<const float2*>(&gate[hh].chi[j]);
-              const float2 lj = *reinterpret_cast<const float2*>(&gate[hh].clo[j]);
+              const float2 lj = PL > 1 ? *reinterpret_cast<const float2*>(&gate[hh].clo[j]) : make_float2(0.f, 0.f);
               float v[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float dh = (e >> 1 ? hi1 : hi0) - (e & 1 ? hj.y : hj.x);
-                const float dl = (e >> 1 ? lo1 : lo0) - (e & 1 ? lj.y : lj.x);
-                const int ahead = i0 + 8 * (e >> 1) - j - (e & 1);  // i - j
-                v[e] = sign * ahead >= 0 ? __uint_as_float(r[4 * nn + e]) * ex2(fsign * (dh + dl)) * scale : 0.f;
+                float d = (e >> 1 ? hi1 : hi0) - (e & 1 ? hj.y : hj.x);
+                if (PL > 1) d += (e >> 1 ? lo1 : lo0) - (e & 1 ? lj.y : lj.x);
+                const bool in = sign * (i0 - j) + sign * (8 * (e >> 1) - (e & 1)) >= 0;
+                v[e] = in ? __uint_as_float(r[4 * nn + e]) * scale * ex2(d) : 0.f;
               }
 #pragma unroll
               for (int p = 0; p < PL; ++p) {
                 if (p >= planes) break;
                 const uint32_t x = bf16x2(v[0], v[1]), y = bf16x2(v[2], v[3]);
-                uint8_t* tile = P + ((g & 1) * L::kPTiles + (PAIR ? hh : p)) * kAtomBytes;
+                uint8_t* tile = tiles + (PAIR ? hh : p) * kAtomBytes;
                 put(tile, i0, j, x);
                 put(tile, i0 + 8, j, y);
                 v[0] -= bf16_lo(x), v[1] -= bf16_hi(x), v[2] -= bf16_lo(y), v[3] -= bf16_hi(y);
               }
             }
           }
+          if (b + 1 < to) {
+            tmem_ld_wait8(next);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = next[i];
+          }
         }
-        tc_fence_before();
-        t.arrive(kS1Free);
         fence_proxy_async();
         t.arrive(kPFull + (g & 1));
       }
@@ -695,7 +723,7 @@ __device__ __forceinline__ void decay_role(const Cta& t) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               v[i] = bf16x2(x[hf][i][0], x[hf][i][1]);
-              x[hf][i][0] -= bf16_lo(v[i]), x[hf][i][1] -= bf16_hi(v[i]);
+              if (p + 1 < kPlanes) x[hf][i][0] -= bf16_lo(v[i]), x[hf][i][1] -= bf16_hi(v[i]);
             }
             tmem_st_16x128_x4(uv + ((uint32_t)(16 * hf) << 16) + 32 * us, v);
           }
@@ -911,6 +939,7 @@ __device__ __forceinline__ void out_role(const Cta& t) {
   const uint32_t lanes = (uint32_t)(32 * q) << 16;
   uint8_t* stage = t.smem + L::kOut + q * kOutBytes;
   uint8_t* dots_in = t.smem + L::kDot + q * kDotBytes;
+  float* sums = reinterpret_cast<float*>(t.smem + L::kSum + q * kSumBytes);
   const int gr = t.lane >> 2, gc = (t.lane & 3) * 2;
   Units walk(t, L::kUnits);
   int g = 0;
@@ -1018,16 +1047,19 @@ __device__ __forceinline__ void out_role(const Cta& t) {
             sum[2 * (m >> 1) + 1] = fmaf(o[hf][2 * m + 1], bf16_hi(v[m]), sum[2 * (m >> 1) + 1]);
           }
         }
+        *reinterpret_cast<float4*>(sums + (b * 32 + t.lane) * 4) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      }
+    }
+    if (dots && active) {
+      // lane 4 r + l of step b has the rows r, r + 8, .. of tokens 16 b + 2 l, + 1, + 8, + 9
+      __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 4);
-          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 8);
-          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
-        }
-        // lanes 0 .. 3 have tokens gc, gc + 1, gc + 8, gc + 9; lane 4 m + l writes the m-th
-        const int m = t.lane >> 2, i = 16 * b + gc + (m & 1) + 8 * (m >> 1);
-        if (m < 4 && i < rows)
-          a.dots[((int64_t)q * a.tokens + tok + i) * a.H + h] = m == 0 ? sum[0] : m == 1 ? sum[1] : m == 2 ? sum[2] : sum[3];
+      for (int k = 0; k < 2; ++k) {
+        const int i = t.lane + 32 * k, b = i >> 4, l = (i & 7) >> 1, e = (i & 1) + 2 * ((i >> 3) & 1);
+        float sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) sum += sums[(b * 32 + 4 * r + l) * 4 + e];
+        if (i < rows) a.dots[((int64_t)q * a.tokens + tok + i) * a.H + h] = sum;
       }
     }
     t.arrive(kGFree + g % kGateSlots);
@@ -1085,7 +1117,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   t.tmem = s_tmem;
 
   // Registers: 896 threads start with 72 each (64512); the warpgroups' shares after the split,
-  // 128 x (40 + 56 + 2 x 56 + 2 x 112 + 72) = 64512, are what the launch holds.
+  // 128 x (40 + 56 + 2 x 64 + 2 x 104 + 72) = 64512, are what the launch holds.
   if (warp < kMaskWarp) {
     set_regs_dec<40>();
     if (warp == kLoadWarp) {
@@ -1101,10 +1133,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     set_regs_dec<56>();
     mask_role<NT, PAIR, PL>(t);
   } else if (warp < kStateWarp) {
-    set_regs_dec<56>();
+    set_regs_dec<64>();
     decay_role<NT, PAIR, PL>(t);
   } else if (warp < kOutWarp) {
-    set_regs_inc<112>();
+    set_regs_inc<104>();
     state_role<NT, PAIR, PL>(t);
   } else if (!states) {
     out_role<NT, PAIR, PL>(t);
