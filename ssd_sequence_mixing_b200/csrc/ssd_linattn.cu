@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
         if (begins) {
           if (a.start) v = a.start[state_at + r * a.sr + c * a.sc];
         } else if (!a.states_only) {
-          v = a.carry[(((int64_t)u * a.H + h) * a.PV + r) * a.NK + c];
+          v = a.carry[(((int64_t)un.window * a.H + h) * a.PV + r) * a.NK + c];
         }
       }
       st[n][e] = v;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
     const int64_t t0 = un.t0 + (int64_t)ci * kLaChunk;
     const int rows = min(kLaChunk, un.len - ci * kLaChunk);
     if (a.dump && a.reverse && (ci == chunks - 1 || ((ci + 1) * kLaChunk) % a.window == 0)) {
-      const int64_t w = un.first_window + ((int64_t)ci * kLaChunk) / a.window;
+      const int64_t w = un.window + ((int64_t)ci * kLaChunk) / a.window;
 #pragma unroll
       for (int n = 0; n < NTILES; ++n)
 #pragma unroll
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
       for (int e = 0; e < 4; ++e) st[n][e] = fmaf(st[n][e], dec, add[n][e]);
 
     if (a.dump && !a.reverse && (ci == chunks - 1 || ((ci + 1) * kLaChunk) % a.window == 0)) {
-      const int64_t w = un.first_window + ((int64_t)ci * kLaChunk) / a.window;
+      const int64_t w = un.window + ((int64_t)ci * kLaChunk) / a.window;
 #pragma unroll
       for (int n = 0; n < NTILES; ++n)
 #pragma unroll
@@ -463,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = r_lo + 8 * (e >> 1), c = 8 * n + gc + (e & 1);
-        if (r < a.PV && c < a.NK) a.carry[(((int64_t)u * a.H + h) * a.PV + r) * a.NK + c] = st[n][e];
+        if (r < a.PV && c < a.NK) a.carry[(((int64_t)un.window * a.H + h) * a.PV + r) * a.NK + c] = st[n][e];
       }
-    if (slice == 0 && threadIdx.x == 0) a.window_decay[(int64_t)u * a.H + h] = (float)exp2(total);
+    if (slice == 0 && threadIdx.x == 0) a.window_decay[(int64_t)un.window * a.H + h] = (float)exp2(total);
     return;
   }
   if (a.last && ends) {
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(256) la_scan_kernel(LaPass a) {
   if (a.win_count && *a.win_count < 0) return;
   constexpr int kV = sizeof(V) / sizeof(float), kBatch = 8;
   const int64_t sh = blockIdx.x;
-  const int seq = (int)(sh / a.H), h = (int)(sh % a.H);
+  const int seq = a.whole + (int)(sh / a.H), h = (int)(sh % a.H);
   const int64_t size = (int64_t)a.PV * a.NK;
   const int w0 = a.cu ? a.first_win[seq] : seq * a.dense_windows;
   const int n = a.cu ? a.first_win[seq + 1] - w0 : a.dense_windows;
@@ -597,7 +597,7 @@ cudaError_t launch_one(const LaPass& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   const int slices = la_general_slices(p.PV);
-  const int64_t units = p.segmented ? p.max_windows : p.nseq;
+  const int64_t units = la_units(p);
   const int64_t blocks = units * p.H * slices;
   if (blocks == 0) return cudaSuccess;
   fn<<<(unsigned)blocks, kThreads, bytes, st>>>(p, slices);
@@ -626,7 +626,7 @@ cudaError_t launch_la_general(const LaPass& p, bool bf16, bool exact, cudaStream
 cudaError_t launch_la_scan(const LaPass& p, cudaStream_t st) {
   const int64_t size = (int64_t)p.PV * p.NK;
   const bool vec = size % 4 == 0;
-  const dim3 grid((unsigned)((int64_t)p.nseq * p.H), (unsigned)((size / (vec ? 4 : 1) + 255) / 256));
+  const dim3 grid((unsigned)((int64_t)(p.nseq - p.whole) * p.H), (unsigned)((size / (vec ? 4 : 1) + 255) / 256));
   if (vec)
     la_scan_kernel<float4><<<grid, 256, 0, st>>>(p);
   else

@@ -49,9 +49,9 @@ struct LaPass {
   const float* start;          // before the first token (reverse: after the last), or null
   float* last;                 // after the last token (reverse: before the first), or null
   int64_t sr, sc;
-  // a CTA's unit is a whole sequence, or (segmented) one window, which starts from
-  // carry[window][H][PV][NK]
-  int segmented;
+  // units: the first `whole` sequences, then the windows of the others, each of which starts from
+  // carry[window][H][PV][NK] (a packed batch has all of its sequences whole, or none)
+  int whole;
   float* carry;                // states_only: the windows' end states from zero go here
   float* window_decay;         // states_only: (window, H) decay over the window
   int states_only;
@@ -64,6 +64,12 @@ struct LaPass {
   int dot_heads, dot_div;
   float* dots;                 // (slices, tokens, H)
 };
+
+inline bool la_segmented(const LaPass& p) { return p.whole < p.nseq; }
+// Upper bound on the units (of one head).
+inline int64_t la_units(const LaPass& p) {
+  return !la_segmented(p) ? p.nseq : p.cu ? p.max_windows : p.whole + (int64_t)(p.nseq - p.whole) * p.dense_windows;
+}
 
 struct LaTable {
   LaWindow* win;

@@ -259,29 +259,44 @@ bool la_aligned(std::initializer_list<const void*> ptrs) {
 
 struct Plan {
   int window, dense_windows, max_windows;
-  bool segmented, table;
+  int whole;  // sequences that are units by themselves; the others' windows are
+  bool table;
+  bool segmented(int64_t rows) const { return whole < rows; }
 };
 
-// Windows.  A sequence runs on `lanes` CTAs of which `resident` fit the GPU at once; where that
-// leaves SMs idle (few sequences and heads, long sequences) it is cut into windows that run side
-// by side, from states that a pass over key and value alone and a scan over the windows give.
-// That pass costs about 0.6 of the full one, so the cut pays where
-// 1.6 * units / resident is below the waves of whole units, with a tenth for the scan.
-Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, int64_t resident) {
+// Windows.  A sequence runs on `lanes` CTAs (of all `passes` together) of which `resident` fit the
+// GPU at once.  Where whole sequences leave SMs idle (few of them, or a last round that is not
+// full) some or all are cut into windows that run side by side, from states that a pass over key
+// and value alone and a scan over the windows give; that pass costs about 0.6 of the full one,
+// and the two launches before it the time of 12 + 4 passes blocks of 64 tokens (30 - 50 us).
+// With k of the sequences of n blocks cut, in blocks' times,
+//   n max(rounds of the others, all the work / resident) + 0.6 n k lanes / resident + 12 + 4 passes
+// and the k with the least is taken.  (2048 tokens: of 8 sequences x 40 pairs of heads one is
+// cut, 306 us instead of 330; of 8 x 32 none.)
+Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, int passes, int64_t resident) {
   const int64_t tokens = s->batch * s->seqlen, rows = cu ? s->nseq : s->batch;
   Plan p{};
   p.window = 512;
-  p.segmented = false;
-  const int64_t mean = rows ? tokens / rows : 0;
-  const double units = (double)rows * (double)lanes;
-  const double waves = (double)((rows * lanes + resident - 1) / resident);
-  // a packed batch may hold one long sequence among short ones: only many sequences fill the
-  // GPU whatever their lengths
-  const bool idle = cu ? units < 4.0 * resident && tokens > 256 : 1.76 * units < waves * resident && mean > 256;
-  if (idle) {
-    p.segmented = true;
+  p.whole = (int)rows;
+  int64_t cut = 0;
+  if (cu) {
+    // a packed batch may hold one long sequence among short ones: only many sequences fill the
+    // GPU whatever their lengths
+    if ((double)rows * (double)lanes < 4.0 * resident && tokens > 256) cut = rows;
+  } else if (s->seqlen > 256) {
+    const double n = (double)((s->seqlen + kLaChunk - 1) / kLaChunk);
+    double best = n * (double)((rows * lanes + resident - 1) / resident);
+    for (int64_t k = 1; k <= std::min<int64_t>(rows, 1024); ++k) {
+      const double work = (double)(rows * lanes) / resident, whole = (double)(((rows - k) * lanes + resident - 1) / resident);
+      const double time = n * std::max(whole, work) + 0.6 * n * (double)(k * lanes) / resident + 12 + 4 * passes;
+      if (time < best) best = time, cut = k;
+    }
+  }
+  if (cut) {
+    p.whole = (int)(rows - cut);
+    const int64_t cut_tokens = cu ? tokens : cut * s->seqlen;
     p.window = 1024;
-    while (p.window > 128 && tokens / p.window * lanes < 3 * resident) p.window /= 2;
+    while (p.window > 128 && cut_tokens / p.window * lanes < resident) p.window /= 2;
   }
   p.dense_windows = (int)std::max<int64_t>(1, (s->seqlen + p.window - 1) / p.window);
   const int64_t most = cu ? tokens / p.window + rows : rows * p.dense_windows;
@@ -294,8 +309,8 @@ Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, int64_t res
 bool wants_tc(const ssd_shape* s) {
   return s->io_dtype == SSD_BF16 && s->headdim % 8 == 0 && s->dstate % 8 == 0 && path_setting() != SSD_PATH_SIMT;
 }
-Plan plan_for(const ssd_shape* s, const int32_t* cu, bool tc, int64_t lanes) {
-  return make_plan(s, cu, lanes, (tc ? 1 : 3) * (int64_t)device_sm_count());
+Plan plan_for(const ssd_shape* s, const int32_t* cu, bool tc, int64_t lanes, int passes) {
+  return make_plan(s, cu, lanes, passes, (tc ? 1 : 3) * (int64_t)device_sm_count());
 }
 
 // Passes over one problem, with the windows' states first where it is segmented: side by side in
@@ -320,7 +335,7 @@ cudaError_t run_passes(LaPass* p, int n, bool tc, bool bf16, float* carry, float
     return e;
   };
   cudaError_t e = cudaSuccess;
-  if (q.segmented) {
+  if (la_segmented(q)) {
     e = launch(own);
     for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_la_scan(p[i], st);
   }
@@ -355,7 +370,7 @@ void set_common(LaPass& p, const ssd_shape* s, const Plan& plan, const int32_t* 
   p.log_decay = log_decay;
   p.per_token = per_token;
   p.scale = scale;
-  p.segmented = plan.segmented;
+  p.whole = plan.whole;
 }
 
 cudaError_t build_table(const ssd_shape* s, const Plan& plan, const int32_t* cu, char* ws, const TableLayout& t,
@@ -386,11 +401,11 @@ extern "C" int ssd_linear_attention_forward(const ssd_shape* s, const void* q, c
   const int P = (int)s->headdim, N = (int)s->dstate, H = (int)s->nheads, hpg = (int)(s->nheads / s->ngroups);
   const bool tc = wants_tc(s);
   if (path_setting() == SSD_PATH_TC && !tc) return SSD_ERR_UNSUPPORTED;
-  const Plan plan = plan_for(s, cu, tc, tc ? (P <= 64 && hpg % 2 == 0 ? H / 2 : H) : H * la_general_slices(P));
+  const Plan plan = plan_for(s, cu, tc, tc ? (P <= 64 && hpg % 2 == 0 ? H / 2 : H) : H * la_general_slices(P), 1);
   const TableLayout tl(plan, rows, 0);
   const size_t o_carry = tl.total;
-  const size_t o_dec = o_carry + (plan.segmented ? up256(sizeof(float) * (size_t)plan.max_windows * H * P * N) : 0);
-  const size_t total = o_dec + (plan.segmented ? up256(sizeof(float) * (size_t)plan.max_windows * H) : 0);
+  const size_t o_dec = o_carry + (plan.segmented(rows) ? up256(sizeof(float) * (size_t)plan.max_windows * H * P * N) : 0);
+  const size_t total = o_dec + (plan.segmented(rows) ? up256(sizeof(float) * (size_t)plan.max_windows * H) : 0);
   char* ws = nullptr;
   if (total && scratch_alloc((void**)&ws, total, st) != cudaSuccess) return SSD_ERR_CUDA;
   LaPass p{};
@@ -435,7 +450,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
   if (path_setting() == SSD_PATH_TC && !tc) return SSD_ERR_UNSUPPORTED;
   const int slices = std::min(la_general_slices(P), la_general_slices(N));
   const int dot_slices = tc && tokens > 0 ? (N + 31) / 32 : la_general_slices(N);  // partial dots of a token
-  const Plan plan = plan_for(s, cu, tc, tc ? 3 * H : H * slices);
+  const Plan plan = plan_for(s, cu, tc, tc ? 3 * H : H * slices, 3);
   const size_t W = (size_t)plan.max_windows, state = (size_t)H * P * N, th = (size_t)tokens * H;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -445,8 +460,8 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
   };
   const TableLayout tl(plan, rows, 0);
   at = tl.total;
-  const size_t o_carry = take(plan.segmented ? 3 * 4 * W * state : 0);
-  const size_t o_dec = take(plan.segmented ? 3 * 4 * W * H : 0);
+  const size_t o_carry = take(plan.segmented(rows) ? 3 * 4 * W * state : 0);
+  const size_t o_dec = take(plan.segmented(rows) ? 3 * 4 * W * H : 0);
   const size_t o_send = take(decay_grad ? 4 * W * state : 0), o_dend = take(decay_grad ? 4 * W * state : 0);
   const size_t o_qdot = take(decay_grad ? 4 * th * dot_slices : 0), o_kdot = take(decay_grad ? 4 * th * dot_slices : 0);
   const size_t o_parts = take(decay_grad && !decay_per_token ? 8 * W * H : 0);

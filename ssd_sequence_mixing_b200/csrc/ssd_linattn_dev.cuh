@@ -21,33 +21,32 @@ __device__ __forceinline__ float exp2_parts(float hi, float lo) { return exp2f(l
 struct Unit {
   int seq;
   int64_t t0;
-  int len, first_window;
+  int len, window;   // window: its number (a whole sequence: that of its first)
   bool first, last;  // the unit begins / ends its sequence
 };
 
 __device__ __forceinline__ bool get_unit(const LaPass& a, int u, Unit& r) {
-  if (a.win_count && (*a.win_count < 0 || (a.segmented && u >= *a.win_count))) return false;
+  const bool whole = u < a.whole;
+  if (a.win_count && (*a.win_count < 0 || (!whole && u >= *a.win_count))) return false;
   int64_t s0, s1;
-  if (!a.segmented) {
+  if (whole) {
     r.seq = u;
     s0 = a.cu ? a.cu[u] : (int64_t)u * a.seqlen;
     s1 = a.cu ? a.cu[u + 1] : s0 + a.seqlen;
     r.t0 = s0;
     r.len = (int)(s1 - s0);
-    r.first_window = a.cu ? (a.first_win ? a.first_win[u] : 0) : u * a.dense_windows;
+    r.window = a.cu ? a.first_win[u] : u * a.dense_windows;
+  } else if (a.cu) {
+    const LaWindow w = a.win[u];
+    r.seq = w.seq, r.t0 = w.t0, r.len = w.len, r.window = u;
+    s0 = a.cu[r.seq], s1 = a.cu[r.seq + 1];
   } else {
-    int idx;
-    if (a.cu) {
-      const LaWindow w = a.win[u];
-      r.seq = w.seq, r.t0 = w.t0, r.len = w.len, idx = w.idx;
-      s0 = a.cu[r.seq], s1 = a.cu[r.seq + 1];
-    } else {
-      r.seq = u / a.dense_windows, idx = u % a.dense_windows;
-      s0 = (int64_t)r.seq * a.seqlen, s1 = s0 + a.seqlen;
-      r.t0 = s0 + (int64_t)idx * a.window;
-      r.len = (int)min((int64_t)a.window, s1 - r.t0);
-    }
-    r.first_window = u;
+    const int v = u - a.whole;
+    r.seq = a.whole + v / a.dense_windows;
+    s0 = (int64_t)r.seq * a.seqlen, s1 = s0 + a.seqlen;
+    r.t0 = s0 + (int64_t)(v % a.dense_windows) * a.window;
+    r.len = (int)min((int64_t)a.window, s1 - r.t0);
+    r.window = a.whole * a.dense_windows + v;
   }
   r.first = r.t0 == s0;
   r.last = r.t0 + r.len == s1;

@@ -76,7 +76,8 @@ enum Bar {
   kYFull = kSpFree + 2, kYFree,
   kGFull, kGFree = kGFull + kGateSlots,
   kUnit = kGFree + kGateSlots, kUnitFree = kUnit + kUnitSlots,  // a unit's description
-  kDrain = kUnitFree + kUnitSlots,  // every product of a warp that issues them is done
+  kDotFull = kUnitFree + kUnitSlots, kDotFree = kDotFull + 2,  // rows that outputs are multiplied with
+  kDrain = kDotFree + 2,  // every product of a warp that issues them is done
   kBars = kDrain + 2
 };
 
@@ -84,7 +85,7 @@ enum Bar {
 struct alignas(16) UnitDesc {
   LaPass a;
   Unit un;
-  int u, h0, chunks, planes, pass;
+  int h0, chunks, planes;
   int begins, ends;
   // The block processed at step c: its place in the unit, its first token and its tokens.
   __device__ __forceinline__ int block(int c) const { return a.reverse ? chunks - 1 - c : c; }
@@ -98,8 +99,8 @@ struct Gate {
 };
 
 // An output warp's own staging: 64 tokens x 32 rows of bf16 at 80 bytes a token, or 16 tokens of
-// fp32 at 144 (neither pitch has bank conflicts); and as much for the rows of the dot products.
-constexpr int kOutPitch = 80, kOutPitch32 = 144, kOutBytes = kC * kOutPitch, kDotBytes = kC * kOutPitch, kSumBytes = 4 * 32 * 16;
+// fp32 at 144 (neither pitch has bank conflicts); and its dot products' parts.
+constexpr int kOutPitch = 80, kOutPitch32 = 144, kOutBytes = kC * kOutPitch, kSumBytes = 4 * 32 * 16;
 
 template <int NT, bool PAIR, int PL>
 struct TcSmem {
@@ -108,10 +109,10 @@ struct TcSmem {
   static constexpr int kHeads = PAIR ? 2 : 1;
   static constexpr int kQ = 0, kK = NT / 64 * kAtomBytes, kV = 2 * kK, kStage = kV + 2 * kAtomBytes;
   static constexpr int kP = kStages * kStage;      // P: two buffers
-  static constexpr int kGate = kP + 2 * kPTiles * kAtomBytes;
+  static constexpr int kDot = kP + 2 * kPTiles * kAtomBytes;  // rows that outputs are multiplied with: two buffers
+  static constexpr int kGate = kDot + (PL > 1 ? 4 : 0) * kAtomBytes;
   static constexpr int kOut = kGate + (int)sizeof(Gate) * kHeads * kGateSlots;  // out warps: staged outputs, ...
-  static constexpr int kDot = kOut + 4 * kOutBytes;                              // ... rows to multiply them with
-  static constexpr int kSum = kDot + (PL > 1 ? 4 * kDotBytes : 0);               // ... and the products' parts
+  static constexpr int kSum = kOut + 4 * kOutBytes;                               // ... and the dot products' parts
   static constexpr int kBar = kSum + (PL > 1 ? 4 * kSumBytes : 0);
   static constexpr int kFlag = kBar + 8 * kBars;
   static constexpr int kUnits = (kFlag + 4 + 15) / 16 * 16;
@@ -217,9 +218,11 @@ __device__ __forceinline__ float exp2_split(double c, float& hi, float& lo) {
 // of heads), walked by a CTA per SM.
 struct TcWork {
   int passes, total;   // total: units of all passes
-  int first[4];        // first unit of each pass
+  // First unit of each pass's whole sequences, and of each pass's windows: the long units come
+  // first, so that the short ones even out the CTAs' shares
+  int first[6];
   int exact[3];        // the pass wants P and S in three planes
-  int8_t map[3][3];    // tensor maps of its query, key and value
+  int8_t map[3][4];    // tensor maps of its query, key, value and dot
   LaPass pass[3];
 };
 struct TcMaps {
@@ -304,20 +307,23 @@ template <int NT, bool PAIR, int PL>
 __device__ __forceinline__ void load_role(const Cta& t, const TcWork& work, const TcMaps& maps) {
   using L = TcSmem<NT, PAIR, PL>;
   UnitDesc* ring = reinterpret_cast<UnitDesc*>(t.smem + L::kUnits);
-  int s = 0, use = 0;  // stage, and its use
+  int s = 0, use = 0, dot = 0;  // stage, and its use; loads of rows for dot products
   bool ok = true, left = true;
 #pragma unroll 1
   for (int n = 0, w = (int)blockIdx.x; ok && left; w += (int)gridDim.x) {
     // the next unit that has work
     left = w < work.total;
-    const int pass = left ? (work.passes > 1 && w >= work.first[1]) + (work.passes > 2 && w >= work.first[2]) : 0;
+    int part = 0;
+#pragma unroll 1
+    for (int i = 1; i < 2 * work.passes; ++i) part += w >= work.first[i];
+    const int pass = part < work.passes ? part : part - work.passes;
     UnitDesc* d = ring + n % kUnitSlots;
     int h0 = 0, chunks = -1;
     Unit un{};
     if (left) {
       const LaPass& a = work.pass[pass];
-      const int rel = w - work.first[pass], per = a.H / L::kHeads;
-      if (!get_unit(a, rel / per, un)) continue;
+      const int rel = w - work.first[part], per = a.H / L::kHeads;
+      if (!get_unit(a, rel / per + (part == pass ? 0 : a.whole), un)) continue;
       const bool ends = a.reverse ? un.first : un.last;
       if (a.states_only && ends) continue;  // nothing follows this window
       h0 = rel % per * L::kHeads, chunks = (un.len + kC - 1) / kC;
@@ -331,7 +337,7 @@ __device__ __forceinline__ void load_role(const Cta& t, const TcWork& work, cons
       for (int i = t.lane; i < (int)(sizeof(LaPass) / 4); i += 32)
         reinterpret_cast<uint32_t*>(&d->a)[i] = reinterpret_cast<const uint32_t*>(&a)[i];
       if (t.lane == 0) {
-        d->un = un, d->u = rel / per, d->h0 = h0, d->planes = work.exact[pass] ? kPlanes : 1;
+        d->un = un, d->h0 = h0, d->planes = work.exact[pass] ? kPlanes : 1;
         d->begins = a.reverse ? un.last : un.first, d->ends = ends;
       }
     } else if (!(ok = t.wait_free(kUnitFree + n % kUnitSlots, n / kUnitSlots))) {
@@ -346,6 +352,9 @@ __device__ __forceinline__ void load_role(const Cta& t, const TcWork& work, cons
     const CUtensorMap *tq = &maps.m[map[0]], *tk = &maps.m[map[1]], *tv = &maps.m[map[2]];
     const int qh = h0 / a.q_div, kh = h0 / a.k_div, vh = h0 / a.v_div;  // (two heads: v_div is 1)
     const bool two = PAIR || a.PV > 64, q = !a.states_only;
+    const bool dots = PL > 1 && a.dots != nullptr;
+    const CUtensorMap* td = &maps.m[map[3]];
+    const int dh = dots ? h0 / a.dot_div : 0;
     const uint32_t bytes = ((q ? 2 : 1) * (NT / 64) + (two ? 2 : 1)) * kAtomBytes;
     const bool reverse = a.reverse;
 #pragma unroll 1
@@ -367,6 +376,20 @@ __device__ __forceinline__ void load_role(const Cta& t, const TcWork& work, cons
       }
       __syncwarp();
       if (++s == L::kStages) s = 0, ++use;
+      if (PL > 1 && dots) {
+        const int slot = dot & 1;
+        if (!(ok = t.wait_free(kDotFree + slot, dot >> 1))) break;
+        if (t.lane == 0) {
+          uint64_t* bar = &t.bars[kDotFull + slot];
+          uint8_t* to = t.smem + L::kDot + slot * 2 * kAtomBytes;
+          const int tok = (int)un.t0 + (reverse ? chunks - 1 - c : c) * kC;
+          mbar_expect_tx(bar, (two ? 2 : 1) * kAtomBytes);
+          tma_load_3d(to, td, 0, dh, tok, bar);
+          if (two) tma_load_3d(to + kAtomBytes, td, 64, dh, tok, bar);
+        }
+        __syncwarp();
+        ++dot;
+      }
     }
   }
   // after a failure: what was issued lands before the CTA ends
@@ -376,6 +399,10 @@ __device__ __forceinline__ void load_role(const Cta& t, const TcWork& work, cons
       const int n = use - (d >= s);  // the last use of stage d that was loaded
       if (n >= 0) wait_polls(smem_u32(&t.bars[kFull + d]), (uint32_t)n & 1u, kDrainPolls);
     }
+  if (PL > 1 && !ok)
+#pragma unroll 1
+    for (int d = max(0, dot - 2); d < dot; ++d)
+      wait_polls(smem_u32(&t.bars[kDotFull + (d & 1)]), (uint32_t)(d >> 1) & 1u, kDrainPolls);
 }
 
 // dS = (upd o value)^T key, plane by plane.
@@ -560,7 +587,7 @@ __device__ __forceinline__ void gate_role(const Cta& t) {
     }
     if (a.states_only && l == 0) {
       float hi, lo;
-      a.window_decay[(int64_t)at.d->u * a.H + at.d->h0 + which] = exp2_split(total, hi, lo);
+      a.window_decay[(int64_t)at.d->un.window * a.H + at.d->h0 + which] = exp2_split(total, hi, lo);
     }
   }
 }
@@ -831,7 +858,7 @@ __device__ __forceinline__ void state_role(const Cta& t) {
     {
       StateAt from{nullptr, a.NK, 1};
       if (!at.d->begins) {
-        if (!states) from = window_at(a.carry, at.d->u);
+        if (!states) from = window_at(a.carry, at.d->un.window);
       } else if (a.start) {
         from = StateAt{const_cast<float*>(a.start) + state_at, a.sr, a.sc};
       }
@@ -881,7 +908,7 @@ __device__ __forceinline__ void state_role(const Cta& t) {
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
           if (!(k ? last : dump)) continue;
-          StateAt to = window_at(k ? a.carry : a.dump, k ? at.d->u : at.d->un.first_window + bl * kC / a.window);
+          StateAt to = window_at(k ? a.carry : a.dump, at.d->un.window + (k ? 0 : bl * kC / a.window));
           if (k && !states) to = StateAt{a.last + state_at, a.sr, a.sc};
           move_state<NC, true>(ds, to, t.lane, row0, n0, a.PV, a.NK);
         }
@@ -938,46 +965,29 @@ __device__ __forceinline__ void out_role(const Cta& t) {
   const int row0 = PAIR ? 32 * q & 63 : 32 * q;  // the warp's first row of the head
   const uint32_t lanes = (uint32_t)(32 * q) << 16;
   uint8_t* stage = t.smem + L::kOut + q * kOutBytes;
-  uint8_t* dots_in = t.smem + L::kDot + q * kDotBytes;
   float* sums = reinterpret_cast<float*>(t.smem + L::kSum + q * kSumBytes);
   const int gr = t.lane >> 2, gc = (t.lane & 3) * 2;
   Units walk(t, L::kUnits);
-  int g = 0;
+  int g = 0, dot = 0;
 #pragma unroll 1
   while (walk.next()) {
   const LaPass& a = walk.d->a;
   const int h = walk.d->h0 + head;
   const bool active = row0 < a.PV;
   const bool dots = PL > 1 && a.dot != nullptr;
-  // The rows that step c's outputs are multiplied with, on their way while its products run.
-  auto fetch_dots = [&](int c) {
-    const int64_t tok = walk.d->token(c);
-    const int rows = walk.d->rows(c);
-    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.dot) + (tok * a.dot_heads + h / a.dot_div) * a.PV + row0;
+  const int PV = a.PV, chunks = walk.d->chunks;
+  const int64_t pitch = (int64_t)a.H * PV;
+  const bool out_f32 = PL > 1 && a.out_f32;
 #pragma unroll 1
-    for (int k = 0; k < 8; ++k) {
-      const int i = 8 * k + (t.lane >> 2), p = (t.lane & 3) * 8;
-      const bool in = i < rows && row0 + p < a.PV;
-      const void* src = in ? from + (int64_t)i * a.dot_heads * a.PV + p : static_cast<const __nv_bfloat16*>(a.dot);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dots_in + i * kOutPitch + p * 2)),
-                   "l"(src), "r"(in ? 16 : 0)
-                   : "memory");
-    }
-    cp_async_commit();
-  };
-#pragma unroll 1
-  for (int c = 0; c < walk.d->chunks; ++c, ++g) {
-    if (dots) fetch_dots(c);
+  for (int c = 0; c < chunks; ++c, ++g) {
     const float* rowf = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (g % kGateSlots) * L::kHeads + head)->row;
     if (!t.wait(kGFull + g % kGateSlots, g / kGateSlots) || !t.wait(kYFull, g)) return;
     tc_fence_after();
     const int64_t tok = walk.d->token(c);
     const int rows = walk.d->rows(c);
-    const int64_t pitch = (int64_t)a.H * a.PV, at = tok * pitch + (int64_t)h * a.PV + row0;
-    if (dots) {
-      cp_async_wait_all();
-      __syncwarp();
-    }
+    const int64_t at = tok * pitch + (int64_t)h * PV + row0;
+    uint8_t* dot_tile = t.smem + L::kDot + (dot & 1) * 2 * kAtomBytes + (row0 >> 6) * kAtomBytes;
+    if (dots && !t.wait(kDotFull + (dot & 1), dot >> 1)) return;
     // Everything is read, and Yi and Ya are free for the next block's products, before anything
     // goes to memory: the products and this reading alternate, and are most of a block's time.
 #pragma unroll 1
@@ -1005,7 +1015,7 @@ __device__ __forceinline__ void out_role(const Cta& t) {
         for (int e = 0; e < 8; ++e)
           o[hf][e] = fmaf(__uint_as_float(yi[hf][e]), e < 4 ? (e & 1 ? f0.y : f0.x) : (e & 1 ? f1.y : f1.x),
                           __uint_as_float(ya[hf][e]));
-      if (PL == 1 || !a.out_f32) {
+      if (PL == 1 || !out_f32) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const uint8_t* to = stage + (16 * b + 8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf + 16 * ((t.lane >> 3) & 1);
@@ -1027,7 +1037,7 @@ __device__ __forceinline__ void out_role(const Cta& t) {
         for (int k = 0; k < 4; ++k) {
           const int i = 4 * k + (t.lane >> 3), p = (t.lane & 7) * 4;
           const float4 v = *reinterpret_cast<const float4*>(stage + i * kOutPitch32 + p * 4);
-          if (16 * b + i < rows && row0 + p < a.PV) *reinterpret_cast<float4*>(to + i * pitch + p) = v;
+          if (16 * b + i < rows && row0 + p < PV) *reinterpret_cast<float4*>(to + i * pitch + p) = v;
         }
         __syncwarp();
       }
@@ -1036,7 +1046,8 @@ __device__ __forceinline__ void out_role(const Cta& t) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t v[4];
-          const uint8_t* from = dots_in + (16 * b + 8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf + 16 * ((t.lane >> 3) & 1);
+          const int i = 16 * b + 8 * (t.lane >> 4) + (t.lane & 7), p = (row0 & 63) + 16 * hf + 8 * ((t.lane >> 3) & 1);
+          const uint8_t* from = dot_tile + sw128_off(i, p >> 3);
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                        : "r"(smem_u32(from))
@@ -1049,6 +1060,10 @@ __device__ __forceinline__ void out_role(const Cta& t) {
         }
         *reinterpret_cast<float4*>(sums + (b * 32 + t.lane) * 4) = make_float4(sum[0], sum[1], sum[2], sum[3]);
       }
+    }
+    if (dots) {
+      t.arrive(kDotFree + (dot & 1));
+      ++dot;
     }
     if (dots && active) {
       // lane 4 r + l of step b has the rows r, r + 8, .. of tokens 16 b + 2 l, + 1, + 8, + 9
@@ -1063,14 +1078,14 @@ __device__ __forceinline__ void out_role(const Cta& t) {
       }
     }
     t.arrive(kGFree + g % kGateSlots);
-    if (!active || (PL > 1 && a.out_f32)) continue;
+    if (!active || out_f32) continue;
     __syncwarp();
     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at;
 #pragma unroll 4
     for (int k = 0; k < 8; ++k) {
       const int i = 8 * k + gr, p = (t.lane & 3) * 8;
       const uint4 v = *reinterpret_cast<const uint4*>(stage + i * kOutPitch + p * 2);
-      if (i < rows && row0 + p < a.PV) *reinterpret_cast<uint4*>(to + i * pitch + p) = v;
+      if (i < rows && row0 + p < PV) *reinterpret_cast<uint4*>(to + i * pitch + p) = v;
     }
     __syncwarp();
   }
@@ -1101,12 +1116,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   if (threadIdx.x >= 32 && threadIdx.x < 32 + kBars) {
     const int i = threadIdx.x - 32;
     int n = 1;
-    if (i == kS1Free || (i >= kPFull && i < kPFree) || i == kYFree) n = 4;
+    if (i == kS1Free || (i >= kPFull && i < kPFree) || i == kYFree || (i >= kDotFree && i < kDrain)) n = 4;
     if ((i >= kReady && i < kFree) || (i >= kUvFull && i < kUvFree)) n = 8;
     if (i == kDsFree || (i >= kSpFull && i < kSpFree)) n = 8;
     if (i >= kFree && i < kS1Full) n = states ? 1 : 2;
     if (i >= kGFree && i < kUnit) n = states ? 20 : 24;
-    if (i >= kUnitFree && i < kDrain) n = states ? 22 : 27;  // every warp but the load warp
+    if (i >= kUnitFree && i < kDotFull) n = states ? 22 : 27;  // every warp but the load warp
     mbar_init(&t.bars[i], n);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1202,15 +1217,18 @@ cudaError_t launch_la_tc(const LaPass* p, int passes, cudaStream_t st) {
   int dims[4] = {}, counts[4] = {}, made = 0;
   work.passes = passes;
   int64_t total = 0;
+  for (int i = 0; i < 2 * passes; ++i) {
+    const LaPass& q = p[i % passes];
+    work.first[i] = (int)std::min<int64_t>(total, INT32_MAX);
+    total += (i < passes ? q.whole : la_units(q) - q.whole) * (pair ? q.H / 2 : q.H);
+  }
   for (int i = 0; i < passes; ++i) {
     work.pass[i] = p[i];
     work.exact[i] = p[i].dots != nullptr;
-    work.first[i] = (int)total;
-    const int64_t units = p[i].segmented ? p[i].max_windows : p[i].nseq;
-    total += units * (pair ? p[i].H / 2 : p[i].H);
-    const void* operand[3] = {p[i].query, p[i].key, p[i].value};
-    const int dim[3] = {p[i].NK, p[i].NK, p[i].PV}, heads[3] = {p[i].q_heads, p[i].k_heads, p[i].v_heads};
-    for (int o = 0; o < 3; ++o) {
+    const void* operand[4] = {p[i].query, p[i].key, p[i].value, p[i].dot};
+    const int dim[4] = {p[i].NK, p[i].NK, p[i].PV, p[i].PV};
+    const int heads[4] = {p[i].q_heads, p[i].k_heads, p[i].v_heads, p[i].dot_heads};
+    for (int o = 0; o < (p[i].dots ? 4 : 3); ++o) {
       int k = 0;
       while (k < made && (bases[k] != operand[o] || dims[k] != dim[o] || counts[k] != heads[o])) ++k;
       if (k == made) {
