@@ -875,10 +875,15 @@ __device__ __forceinline__ void state_role(const Cta& t) {
         if (!t.wait(kDsFull, g)) return;
       }
       const bool more = c + 1 < at.d->chunks, out = more && !states;
-      const int slot = m % sp_slots;  // the next step's first plane goes out as S is made
+      // The next step's first plane goes out as S is made, and of three the second with it; the
+      // third follows when the first one's slot is free again.
+      const bool three = PL > 1 && planes > 1;
+      const int slot = m % sp_slots, slot2 = (m + 1) % sp_slots;
       if (out && !t.wait_free(kSpFree + slot, m / sp_slots)) return;
+      if (PL > 1 && out && three && !t.wait_free(kSpFree + slot2, (m + 1) / sp_slots)) return;
       tc_fence_after();
       const uint32_t sp = t.tmem + lanes + (slot ? kColSp1 : kColSp0) + half * (NC / 2);
+      const uint32_t sp2 = t.tmem + lanes + (slot2 ? kColSp1 : kColSp0) + half * (NC / 2);
 #pragma unroll
       for (int b = 0; b < NC / 16; ++b) {
         uint32_t d[16], v[8];
@@ -889,6 +894,12 @@ __device__ __forceinline__ void state_role(const Cta& t) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = bf16x2(S[16 * b + 2 * i], S[16 * b + 2 * i + 1]);
         if (out) tmem_st8(sp + 8 * b, v);
+        if (PL > 1 && out && three) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = bf16x2(S[16 * b + 2 * i] - bf16_lo(v[i]), S[16 * b + 2 * i + 1] - bf16_hi(v[i]));
+          tmem_st8(sp2 + 8 * b, v);
+        }
       }
       if (out) tmem_st_wait();
       // Copies that are wanted: of the windows' states (forward, after a window's last block;
@@ -916,39 +927,38 @@ __device__ __forceinline__ void state_role(const Cta& t) {
       tc_fence_before();
       if (out) {
         t.arrive(kSpFull + slot);
-        ++m;
+        if (PL > 1 && three) t.arrive(kSpFull + slot2);
+        m += PL > 1 && three ? 2 : 1;
       }
       if (more) t.arrive(kDsFree);
       if (c >= 0) {
         t.arrive(kGFree + g % kGateSlots);
         ++g;
       }
-      if (PL > 1 && out) {  // the planes of what the first one leaves
-#pragma unroll 1
-        for (int p = 1; p < planes; ++p, ++m) {
-          const int sl = m % sp_slots;
-          if (!t.wait_free(kSpFree + sl, m / sp_slots)) return;
-          tc_fence_after();
-          const uint32_t to = t.tmem + lanes + (sl ? kColSp1 : kColSp0) + half * (NC / 2);
+      if (PL > 1 && out && three) {  // what the first two leave
+        const int sl = m % sp_slots;
+        if (!t.wait_free(kSpFree + sl, m / sp_slots)) return;
+        tc_fence_after();
+        const uint32_t to = t.tmem + lanes + (sl ? kColSp1 : kColSp0) + half * (NC / 2);
 #pragma unroll
-          for (int b = 0; b < NC / 16; ++b) {
-            uint32_t v[8];
+        for (int b = 0; b < NC / 16; ++b) {
+          uint32_t v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              // made anew for each plane: kept across them, the remainders would not fit the registers
-              asm volatile("" : "+f"(S[16 * b + 2 * i]), "+f"(S[16 * b + 2 * i + 1]));
-              float x = S[16 * b + 2 * i], y = S[16 * b + 2 * i + 1];
-              v[i] = bf16x2(x, y);
-              x -= bf16_lo(v[i]), y -= bf16_hi(v[i]);
-              v[i] = bf16x2(x, y);
-              if (p > 1) v[i] = bf16x2(x - bf16_lo(v[i]), y - bf16_hi(v[i]));
-            }
-            tmem_st8(to + 8 * b, v);
+          for (int i = 0; i < 8; ++i) {
+            // made anew: kept from above, the remainders would not fit the registers
+            asm volatile("" : "+f"(S[16 * b + 2 * i]), "+f"(S[16 * b + 2 * i + 1]));
+            float x = S[16 * b + 2 * i], y = S[16 * b + 2 * i + 1];
+            v[i] = bf16x2(x, y);
+            x -= bf16_lo(v[i]), y -= bf16_hi(v[i]);
+            v[i] = bf16x2(x, y);
+            v[i] = bf16x2(x - bf16_lo(v[i]), y - bf16_hi(v[i]));
           }
-          tmem_st_wait();
-          tc_fence_before();
-          t.arrive(kSpFull + sl);
+          tmem_st8(to + 8 * b, v);
         }
+        tmem_st_wait();
+        tc_fence_before();
+        t.arrive(kSpFull + sl);
+        ++m;
       }
     }
   }
@@ -957,7 +967,7 @@ __device__ __forceinline__ void state_role(const Cta& t) {
 // Yi, Ya -> out: warp q writes rows 32 q .., 16 tokens at a time.  Tensor memory is read in the layout of mma.sync's accumulators (registers are pairs of
 // tokens of one row), turned by transposing stores to shared memory, and written from there
 // in 16-byte pieces (single 2-byte stores took 16 cycles each, 5 of a block's 9 thousand).
-template <int NT, bool PAIR, int PL>
+template <int NT, bool PAIR, int PL, bool F32>
 __device__ __forceinline__ void out_role(const Cta& t) {
   using L = TcSmem<NT, PAIR, PL>;
   const int q = threadIdx.x / 32 & 3;
@@ -977,7 +987,7 @@ __device__ __forceinline__ void out_role(const Cta& t) {
   const bool dots = PL > 1 && a.dot != nullptr;
   const int PV = a.PV, chunks = walk.d->chunks;
   const int64_t pitch = (int64_t)a.H * PV;
-  const bool out_f32 = PL > 1 && a.out_f32;
+  const bool out_f32 = F32 && a.out_f32;
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c, ++g) {
     const float* rowf = (reinterpret_cast<const Gate*>(t.smem + L::kGate) + (g % kGateSlots) * L::kHeads + head)->row;
@@ -1015,7 +1025,7 @@ __device__ __forceinline__ void out_role(const Cta& t) {
         for (int e = 0; e < 8; ++e)
           o[hf][e] = fmaf(__uint_as_float(yi[hf][e]), e < 4 ? (e & 1 ? f0.y : f0.x) : (e & 1 ? f1.y : f1.x),
                           __uint_as_float(ya[hf][e]));
-      if (PL == 1 || !out_f32) {
+      if (!out_f32) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const uint8_t* to = stage + (16 * b + 8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf + 16 * ((t.lane >> 3) & 1);
@@ -1094,7 +1104,7 @@ __device__ __forceinline__ void out_role(const Cta& t) {
 
 // Grid: a CTA per SM at most; CTA b takes units b, b + grid, ... of the list (units of a pass times
 // heads or pairs of heads, heads fastest).
-template <int NT, bool PAIR, int PL>
+template <int NT, bool PAIR, int PL, bool F32>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     la_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcWork work, unsigned int* status,
                  uint32_t polls, int withhold) {
@@ -1154,7 +1164,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     set_regs_inc<104>();
     state_role<NT, PAIR, PL>(t);
   } else if (!states) {
-    out_role<NT, PAIR, PL>(t);
+    out_role<NT, PAIR, PL, F32>(t);
   }
 
   __syncwarp();
@@ -1180,9 +1190,9 @@ bool make_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t toke
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, bool PAIR, int PL>
+template <int NT, bool PAIR, int PL, bool F32>
 cudaError_t launch_one(const TcMaps& maps, const TcWork& work, cudaStream_t st) {
-  auto* fn = la_tc_kernel<NT, PAIR, PL>;
+  auto* fn = la_tc_kernel<NT, PAIR, PL, F32>;
   using L = TcSmem<NT, PAIR, PL>;
   static_assert(L::kBytes <= 227 * 1024, "tiles must fit the SM's shared memory");
   static_assert(kBars + 32 <= kThreadsTc, "a thread per barrier");
@@ -1205,12 +1215,13 @@ bool la_tc_pairs(const LaPass& p) {
 }
 
 cudaError_t launch_la_tc(const LaPass* p, int passes, cudaStream_t st) {
-  bool exact = false, pair = passes == 1 && la_tc_pairs(p[0]), narrow = true;
+  bool exact = false, f32 = false, pair = passes == 1 && la_tc_pairs(p[0]), narrow = true;
   for (int i = 0; i < passes; ++i) {
-    exact |= p[i].dots != nullptr || p[i].out_f32;  // (only that instance writes fp32)
+    exact |= p[i].dots != nullptr;
+    f32 |= p[i].out_f32 != 0;
     narrow &= p[i].NK <= 64;
   }
-  pair &= !exact;
+  pair &= !exact && !f32;
   TcWork work{};
   TcMaps maps;
   const void* bases[4] = {};  // an operand that passes share has one map
@@ -1243,9 +1254,13 @@ cudaError_t launch_la_tc(const LaPass* p, int passes, cudaStream_t st) {
   if (total > (1ll << 31) - 1) return cudaErrorInvalidConfiguration;
   if (total == 0) return cudaSuccess;
   work.total = (int)total;
-  if (exact) return narrow ? launch_one<64, false, kPlanes>(maps, work, st) : launch_one<128, false, kPlanes>(maps, work, st);
-  if (pair) return narrow ? launch_one<64, true, 1>(maps, work, st) : launch_one<128, true, 1>(maps, work, st);
-  return narrow ? launch_one<64, false, 1>(maps, work, st) : launch_one<128, false, 1>(maps, work, st);
+  if (exact && f32)
+    return narrow ? launch_one<64, false, kPlanes, true>(maps, work, st) : launch_one<128, false, kPlanes, true>(maps, work, st);
+  if (exact)
+    return narrow ? launch_one<64, false, kPlanes, false>(maps, work, st) : launch_one<128, false, kPlanes, false>(maps, work, st);
+  if (f32) return narrow ? launch_one<64, false, 1, true>(maps, work, st) : launch_one<128, false, 1, true>(maps, work, st);
+  if (pair) return narrow ? launch_one<64, true, 1, false>(maps, work, st) : launch_one<128, true, 1, false>(maps, work, st);
+  return narrow ? launch_one<64, false, 1, false>(maps, work, st) : launch_one<128, false, 1, false>(maps, work, st);
 }
 
 }  // namespace ssd
