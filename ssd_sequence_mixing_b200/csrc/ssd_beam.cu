@@ -5,14 +5,15 @@
 // are scores[i] + (x[i,w] - lse_i); the best `count` over all (i, w) are wanted, ties to the
 // lowest i * vocab + w.  The logits are read once:
 //   1. blocks of 256 threads, several to a row of logits.  A thread goes over its elements
-//      once and keeps their running maximum, its place, and the running sum of exp(x - R) with
-//      R a multiple of 128 near the maximum.  Each term is a function of x alone (R is the same
-//      for all of a usual row) and the sum is held in 64 bits, so equal rows have equal sums
-//      however they are cut among threads, and equal scores tie.  Let K be the count-th best of the threads' maxima: an element among
-//      the row's best is at or above K and belongs to one of the `count` threads whose maximum
-//      is (count other threads would otherwise each hold a better one), so those threads alone
-//      go over their elements (some dozens, still in cache) a second time and hand on what is
-//      at or above K.
+//      once, four vectors of 16 bytes in flight, and keeps their running maximum, its place,
+//      and the running sum of exp(x - R) with R a multiple of 128 near the maximum.  Each term
+//      is a function of x alone (R is the same for all of a usual row) and the sum is held in
+//      64 bits, so equal rows have equal sums however they are cut among threads, and equal
+//      scores tie.  Let K be the count-th best of the threads' maxima: an element among the
+//      row's best is at or above K and belongs to one of the `count` threads whose maximum is
+//      (count other threads would otherwise each hold a better one), so those threads alone go
+//      over their elements (some dozens, still in cache) a second time and hand on what is at
+//      or above K.
 //   2. one block per batch item joins the sums, forms the scores in 64 bits and picks the best
 //      of the rows' sorted lists by the same argument.
 // Bound by HBM on the logits for large batches, by the two launches' latency for one row.
@@ -116,15 +117,17 @@ __device__ __forceinline__ int rank_of(uint64_t mine, const uint64_t* keys, int 
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
-  constexpr int n = Vec<T>::n;
+  constexpr int n = Vec<T>::n, kVecs = 4, kWarps = kThreads / 32;
   extern __shared__ uint64_t s_list[];  // count * elements per thread
   __shared__ uint64_t s_key[kThreads];
-  __shared__ double s_sum[kThreads / 32];
-  __shared__ float s_max[kThreads / 32];
+  __shared__ uint64_t s_sorted[kWarps][32];  // each warp's best keys, in order
+  __shared__ double s_sum[kWarps];
+  __shared__ float s_max[kWarps];
   __shared__ uint64_t s_limit;
   __shared__ int s_n;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / a.splits;
+  if (a.finished && a.finished[row]) return;  // its logits do not matter
   const int split = blockIdx.x % a.splits;
   const T* logits = static_cast<const T*>(a.logits);
   const int64_t start = row * a.vocab;  // of the row in the flat array
@@ -134,17 +137,22 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
 
   float m = -INFINITY, R = -INFINITY;
   double s = 0.0;
-  int64_t best = -1;
-  for (int64_t j = j0 + tid; j < j1; j += kThreads) {
-    float x[n];
-    load_vec(logits, j, lo, hi, x);
-    float top = x[0];
+  int best = -1;  // place of the maximum in the row
+  for (int64_t j = j0 + tid; j < j1; j += kVecs * kThreads) {
+    float x[kVecs][n];
 #pragma unroll
-    for (int i = 1; i < n; ++i) top = fmaxf(top, x[i]);
+    for (int v = 0; v < kVecs; ++v) load_vec(logits, j + v * kThreads, lo, hi, x[v]);  // (past the range: -inf)
+    float top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int i = 0; i < n; ++i) top = fmaxf(top, x[v][i]);
     if (top > m) {
 #pragma unroll
-      for (int i = n - 1; i >= 0; --i)
-        if (x[i] == top) best = j * n + i;
+      for (int v = kVecs - 1; v >= 0; --v)
+#pragma unroll
+        for (int i = n - 1; i >= 0; --i)
+          if (x[v][i] == top) best = (int)((j + v * kThreads) * n + i - start);
       m = top;
       if (top - R > 64.f) {  // the first value, or a far larger one
         const float to = 128.f * rintf(top * (1.f / 128.f));
@@ -154,24 +162,33 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
     }
     const float ref = R == -INFINITY ? 0.f : R;
 #pragma unroll
-    for (int i = 0; i < n; ++i) s += (double)exp_term(x[i] - ref);  // NaN from an infinite or NaN logit on
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int i = 0; i < n; ++i) s += (double)exp_term(x[v][i] - ref);  // NaN from an infinite or NaN logit on
   }
   // a thread without an element above -inf has no key
-  const uint64_t mine = best >= 0 ? key_of(m, (uint32_t)(best - start)) : 0;
+  const uint64_t mine = best >= 0 ? key_of(m, (uint32_t)best) : 0;
   float bm = R;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
   if (lane == 0) s_max[warp] = bm;
   s_key[tid] = mine;
+  s_sorted[warp][lane] = 0;
   if (tid == 0) s_n = 0, s_limit = 1;
+  __syncwarp();
+  int r = mine ? rank_of(mine, s_key + 32 * warp, 32) : kThreads;  // in the warp
+  if (mine) s_sorted[warp][r] = mine;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) bm = fmaxf(bm, s_max[w]);
+  for (int w = 0; w < kWarps; ++w) bm = fmaxf(bm, s_max[w]);
   double sum = s == 0.0 ? 0.0 : s * exp((double)R - (double)bm);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
-  const int r = mine ? rank_of(mine, s_key, kThreads) : kThreads;
+  if (mine && r < a.count)  // ... and in the block, from the other warps' lists
+    for (int w = 0; w < kWarps && r < a.count; ++w)
+      if (w != warp)
+        for (int i = 0; i < 32 && r < a.count && s_sorted[w][i] > mine; ++i) ++r;
   if (r == a.count - 1) s_limit = mine;
   __syncthreads();
   if (r < a.count) {
@@ -199,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
   if (tid == 0) {
     double t = 0.0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) t += s_sum[w];
+    for (int w = 0; w < kWarps; ++w) t += s_sum[w];
     a.row_ref[blockIdx.x] = bm;
     a.row_sum[blockIdx.x] = t;
   }
@@ -246,6 +263,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(Select a) {
   const int64_t list0 = b * lists;
   if (tid == 0) s_n = 0, s_limit = Cand{1, 0xFFFFFFFFu, 0};
   for (int i = tid; i < a.beams; i += kThreads) {
+    if (a.finished && a.finished[b * a.beams + i]) continue;  // (nothing was written for it)
     float m = -INFINITY;
     for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.row_ref[list0 + i * a.splits + s]);
     double sum = 0.0;
