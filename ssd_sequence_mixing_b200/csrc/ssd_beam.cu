@@ -78,17 +78,23 @@ struct Vec {
   T v[n];
 };
 
-// Elements [8 j, 8 j + 8) (fp32: 4) of the flat logits, those outside [lo, hi) as -inf.
+// Elements [8 j, 8 j + 8) (fp32: 4) of the flat logits.
+template <typename T>
+__device__ __forceinline__ void load_whole(const T* logits, int64_t j, float (&x)[Vec<T>::n]) {
+  Vec<T> v;
+  *reinterpret_cast<uint4*>(&v) = __ldg(reinterpret_cast<const uint4*>(logits) + j);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::n; ++i) x[i] = to_f(v.v[i]);
+}
+
+// The same, those outside [lo, hi) as -inf.
 template <typename T>
 __device__ __forceinline__ void load_vec(const T* logits, int64_t j, int64_t lo, int64_t hi,
                                          float (&x)[Vec<T>::n]) {
   constexpr int n = Vec<T>::n;
   const int64_t e0 = j * n;
   if (e0 >= lo && e0 + n <= hi) {
-    Vec<T> v;
-    *reinterpret_cast<uint4*>(&v) = __ldg(reinterpret_cast<const uint4*>(logits) + j);
-#pragma unroll
-    for (int i = 0; i < n; ++i) x[i] = to_f(v.v[i]);
+    load_whole(logits, j, x);
   } else {  // the range begins or ends inside this vector
 #pragma unroll
     for (int i = 0; i < n; ++i) x[i] = e0 + i >= lo && e0 + i < hi ? to_f(logits[e0 + i]) : -INFINITY;
@@ -123,6 +129,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
   __shared__ uint64_t s_sorted[kWarps][32];  // each warp's best keys, in order
   __shared__ double s_sum[kWarps];
   __shared__ float s_max[kWarps];
+  __shared__ int s_who[kMaxBeams];  // the threads with the best maxima, in order
   __shared__ uint64_t s_limit;
   __shared__ int s_n;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -135,25 +142,28 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
   const int64_t hi = min(start + a.vocab, lo + a.per_split);
   const int64_t j0 = lo / n, j1 = (hi + n - 1) / n;  // 16-byte vectors that hold the range
 
+  // vectors of the block: [0, vecs), those that lie in the range as a whole: [in0, in1)
+  const int vecs = (int)(j1 - j0), in0 = lo % n != 0, in1 = (int)(hi / n - j0);
   float m = -INFINITY, R = -INFINITY;
   double s = 0.0;
-  int best = -1;  // place of the maximum in the row
-  for (int64_t j = j0 + tid; j < j1; j += kVecs * kThreads) {
+  int from = 0;  // the group of vectors that holds the maximum first
+  for (int u = tid; u < vecs; u += kVecs * kThreads) {
     float x[kVecs][n];
+    if (u >= in0 && u + (kVecs - 1) * kThreads < in1) {
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) load_vec(logits, j + v * kThreads, lo, hi, x[v]);  // (past the range: -inf)
+      for (int v = 0; v < kVecs; ++v) load_whole(logits, j0 + u + v * kThreads, x[v]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) load_vec(logits, j0 + u + v * kThreads, lo, hi, x[v]);  // (past the range: -inf)
+    }
     float top = -INFINITY;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
       for (int i = 0; i < n; ++i) top = fmaxf(top, x[v][i]);
     if (top > m) {
-#pragma unroll
-      for (int v = kVecs - 1; v >= 0; --v)
-#pragma unroll
-        for (int i = n - 1; i >= 0; --i)
-          if (x[v][i] == top) best = (int)((j + v * kThreads) * n + i - start);
       m = top;
+      from = u;
       if (top - R > 64.f) {  // the first value, or a far larger one
         const float to = 128.f * rintf(top * (1.f / 128.f));
         s *= exp((double)R - (double)to);
@@ -166,6 +176,17 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
 #pragma unroll
       for (int i = 0; i < n; ++i) s += (double)exp_term(x[v][i] - ref);  // NaN from an infinite or NaN logit on
   }
+  int best = -1;  // place of the maximum in the row
+  if (m > -INFINITY) {  // looked up once: at every new maximum it cost a quarter of the loop
+#pragma unroll
+    for (int v = kVecs - 1; v >= 0; --v) {
+      float x[n];
+      load_vec(logits, j0 + from + v * kThreads, lo, hi, x);
+#pragma unroll
+      for (int i = n - 1; i >= 0; --i)
+        if (x[i] == m) best = (int)((j0 + from + v * kThreads) * n + i - start);
+    }
+  }
   // a thread without an element above -inf has no key
   const uint64_t mine = best >= 0 ? key_of(m, (uint32_t)best) : 0;
   float bm = R;
@@ -174,6 +195,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
   if (lane == 0) s_max[warp] = bm;
   s_key[tid] = mine;
   s_sorted[warp][lane] = 0;
+  if (tid < kMaxBeams) s_who[tid] = -1;
   if (tid == 0) s_n = 0, s_limit = 1;
   __syncwarp();
   int r = mine ? rank_of(mine, s_key + 32 * warp, 32) : kThreads;  // in the warp
@@ -190,10 +212,13 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
       if (w != warp)
         for (int i = 0; i < 32 && r < a.count && s_sorted[w][i] > mine; ++i) ++r;
   if (r == a.count - 1) s_limit = mine;
+  if (r < a.count) s_who[r] = tid;
   __syncthreads();
-  if (r < a.count) {
-    const uint64_t limit = s_limit;
-    for (int64_t j = j0 + tid; j < j1; j += kThreads) {
+  // a warp takes all vectors of one such thread at once
+  const uint64_t limit = s_limit;
+  for (int q = warp; q < a.count; q += kWarps) {
+    if (s_who[q] < 0) break;
+    for (int64_t j = j0 + s_who[q] + lane * kThreads; j < j1; j += 32 * kThreads) {
       float x[n];
       load_vec(logits, j, lo, hi, x);
 #pragma unroll
@@ -258,21 +283,30 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(Select a) {
   Cand* s_cand = s_head + lists;                                   // count * count
   __shared__ Cand s_limit;
   __shared__ int s_n;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.x;
   const int64_t list0 = b * lists;
   if (tid == 0) s_n = 0, s_limit = Cand{1, 0xFFFFFFFFu, 0};
-  for (int i = tid; i < a.beams; i += kThreads) {
+  for (int i = warp; i < a.beams; i += kThreads / 32) {  // a warp per beam, a lane or more per split
     if (a.finished && a.finished[b * a.beams + i]) continue;  // (nothing was written for it)
-    float m = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.row_ref[list0 + i * a.splits + s]);
-    double sum = 0.0;
-    for (int s = 0; s < a.splits; ++s) {
-      const int64_t l = list0 + i * a.splits + s;
-      const double part = a.row_sum[l];
-      if (part != 0.0) sum += part * exp((double)a.row_ref[l] - (double)m);
+    static_assert(kMaxSplits <= 64, "a lane takes two splits");
+    float ref[2], m = -INFINITY;
+    double part[2], sum = 0.0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int e = lane + 32 * h;
+      ref[h] = e < a.splits ? a.row_ref[list0 + i * a.splits + e] : -INFINITY;
+      part[h] = e < a.splits ? a.row_sum[list0 + i * a.splits + e] : 0.0;
+      m = fmaxf(m, ref[h]);
     }
-    s_lse[i] = (double)m + log(sum);  // a row of -inf alone: -inf + -inf, and no key to use it
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (part[h] != 0.0) sum += part[h] * exp((double)ref[h] - (double)m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_lse[i] = (double)m + log(sum);  // a row of -inf alone: -inf + -inf, and no key to use it
   }
   for (int i = tid; i < a.count; i += kThreads) {  // what stays where there are too few continuations
     a.out_scores[b * a.count + i] = -INFINITY;
@@ -297,16 +331,14 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(Select a) {
   }
   __syncthreads();
   const Cand limit = s_limit;
-  for (int l = tid; l < lists; l += kThreads) {
+  for (int q = tid; q < lists * a.count; q += kThreads) {  // all entries at once: one load's latency
+    const int l = q / a.count, e = q - l * a.count;
     if (!s_head[l].score || before(limit, s_head[l])) continue;  // below the limit from the start
     const int beam = l / a.splits;
     const bool fin = a.finished && a.finished[b * a.beams + beam];
-    for (int e = 0; e < a.count; ++e) {
-      const Cand c = candidate(a, a.keys + (list0 + l) * a.count, beam, l % a.splits == 0, e, s_lse[beam],
-                               (double)a.scores[b * a.beams + beam], fin);
-      if (!c.score || before(limit, c)) break;
-      s_cand[atomicAdd(&s_n, 1)] = c;
-    }
+    const Cand c = candidate(a, a.keys + (list0 + l) * a.count, beam, l % a.splits == 0, e, s_lse[beam],
+                             (double)a.scores[b * a.beams + beam], fin);
+    if (c.score && !before(limit, c)) s_cand[atomicAdd(&s_n, 1)] = c;
   }
   __syncthreads();
   const int got = s_n;
