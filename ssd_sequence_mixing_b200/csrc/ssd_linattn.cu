@@ -134,6 +134,10 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
   extern __shared__ __align__(16) unsigned char smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   constexpr int KS = NT / 16, NTILES = NT / 8;
+  // fp32 operands: the products of lower planes have accumulators of their own.  An accumulation
+  // in the tensor core truncates to the sum's last bit, and the sum of the highest planes
+  // then takes a sixth of them.
+  constexpr bool kLow = SP == 3;
   const int slice = blockIdx.x % slices;
   const int h = (blockIdx.x / slices) % a.H;
   const int u = blockIdx.x / slices / a.H;
@@ -148,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
   const int gr = lane >> 2, gc = (lane & 3) * 2;
   const int row0 = slice * kLaSlice;          // first value row of the CTA
   const int r_lo = row0 + 16 * warp + gr;     // this thread's value rows: r_lo, r_lo + 8
+  const bool has_rows = row0 + 16 * warp < a.PV;  // (a warp without any still computes rows of P)
   const int qh = h / a.q_div, kh = h / a.k_div, vh = h / a.v_div;
   const int64_t state_at = ((int64_t)un.seq * a.H + h) * a.NK * a.PV;
 
@@ -227,14 +232,28 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
     if (!a.states_only) {
       // P = decay o (query key^T) * scale: warp's rows i = 16 warp .., all columns j
       const int i_lo = 16 * warp + gr;
-      float acc[8][4];
+      float acc[8][4], low[kLow ? 8 : 1][4];
+      auto clear = [&]() {
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+        for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) {
+            acc[n][e] = 0.f;
+            if constexpr (kLow) low[n][e] = 0.f;
+          }
+      };
+      auto join = [&]() {
+        if constexpr (kLow)
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] += low[n][e];
+      };
+      clear();
       const int n0 = a.reverse ? 2 * warp : 0, n1 = a.reverse ? 8 : 2 * warp + 2;  // column tiles with any j in reach
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
+        if (16 * ks >= a.NK) continue;
         uint32_t qa[SP][4];
 #pragma unroll
         for (int p = 0; p < SP; ++p)
@@ -250,11 +269,12 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
           for (int i = SP - 1; i >= 0; --i)
 #pragma unroll
             for (int j = SP - 1 - i; j >= 0; --j) {
-              mma(acc[n], qa[i], kb[j][0], kb[j][1]);
-              mma(acc[n + 1], qa[i], kb[j][2], kb[j][3]);
+              mma(kLow && i + j ? low[kLow ? n : 0] : acc[n], qa[i], kb[j][0], kb[j][1]);
+              mma(kLow && i + j ? low[kLow ? n + 1 : 0] : acc[n + 1], qa[i], kb[j][2], kb[j][3]);
             }
         }
       }
+      join();
       const float hi0 = sm.chi[i_lo], lo0 = sm.clo[i_lo], hi1 = sm.chi[i_lo + 8], lo1 = sm.clo[i_lo + 8];
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
@@ -280,12 +300,10 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
       __syncthreads();
 
       // out^T (16 value rows of the warp x 64 tokens) = row o (S query^T) + value^T P^T
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+      clear();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
+        if (16 * ks >= a.NK || !has_rows) continue;
         uint32_t sa[4][PO];
         split2<PO>(st[2 * ks][0], st[2 * ks][1], sa[0]);
         split2<PO>(st[2 * ks][2], st[2 * ks][3], sa[1]);
@@ -303,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
 #pragma unroll
             for (int j = SP - 1; j >= 0; --j) {
               if (i + j > 2) continue;
-              mma(acc[n], af, qb[j][0], qb[j][1]);
-              mma(acc[n + 1], af, qb[j][2], qb[j][3]);
+              mma(kLow && i + j ? low[kLow ? n : 0] : acc[n], af, qb[j][0], qb[j][1]);
+              mma(kLow && i + j ? low[kLow ? n + 1 : 0] : acc[n + 1], af, qb[j][2], qb[j][3]);
             }
           }
         }
@@ -312,9 +330,13 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
 #pragma unroll
       for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] *= sm.row[8 * n + gc + (e & 1)];
+        for (int e = 0; e < 4; ++e) {
+          acc[n][e] *= sm.row[8 * n + gc + (e & 1)];
+          if constexpr (kLow) low[n][e] *= sm.row[8 * n + gc + (e & 1)];
+        }
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
+        if (!has_rows) continue;
         uint32_t va[SP][4];
 #pragma unroll
         for (int p = 0; p < SP; ++p)
@@ -332,11 +354,12 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
 #pragma unroll
             for (int j = PO - 1; j >= 0; --j) {
               if (i + j > 2) continue;
-              mma(acc[n], va[i], pb[j][0], pb[j][1]);
-              mma(acc[n + 1], va[i], pb[j][2], pb[j][3]);
+              mma(kLow && i + j ? low[kLow ? n : 0] : acc[n], va[i], pb[j][0], pb[j][1]);
+              mma(kLow && i + j ? low[kLow ? n + 1 : 0] : acc[n + 1], va[i], pb[j][2], pb[j][3]);
             }
         }
       }
+      join();
       // acc[n][e]: value row r_lo + 8 (e >> 1), token 8 n + gc + (e & 1)
       if (a.dot) {
         const int64_t dp = (int64_t)a.dot_heads * a.PV;
@@ -400,51 +423,65 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
 
     // S <- 2^(c_end) S + (upd o value)^T key, the sum over the block in accumulators of its
     // own: adding 64 tokens at a time in fp32 keeps the tensor core's truncating accumulation
-    // from piling up over a long memory.
+    // from piling up over a long memory.  fp32 operands go by halves of the columns, whose
+    // two sets of accumulators fit the registers.
     const float dec = sm.decay;
-    float add[NTILES][4];
+    constexpr int kPart = kLow ? NTILES / 2 : NTILES;
 #pragma unroll
-    for (int n = 0; n < NTILES; ++n)
+    for (int part = 0; part < NTILES; part += kPart) {
+      if (8 * part >= a.NK || !has_rows) continue;
+      float add[kPart][4], low[kLow ? kPart : 1][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) add[n][e] = 0.f;
+      for (int n = 0; n < kPart; ++n)
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      uint32_t va[SP][4];
+        for (int e = 0; e < 4; ++e) {
+          add[n][e] = 0.f;
+          if constexpr (kLow) low[n][e] = 0.f;
+        }
 #pragma unroll
-      for (int p = 0; p < SP; ++p)
-        ldsm4t(va[p], &sm.v[p][16 * kk + (lane & 7) + ((lane >> 4) & 1) * 8][16 * warp + ((lane >> 3) & 1) * 8]);
-      const float u0 = sm.upd[16 * kk + gc], u1 = sm.upd[16 * kk + gc + 1];
-      const float u2 = sm.upd[16 * kk + gc + 8], u3 = sm.upd[16 * kk + gc + 9];
-      uint32_t ua[4][3];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        float x = 0.f, y = 0.f;
-#pragma unroll
-        for (int p = SP - 1; p >= 0; --p) x += sm100::bf16_lo(va[p][m]), y += sm100::bf16_hi(va[p][m]);
-        split2<3>(x * (m < 2 ? u0 : u2), y * (m < 2 ? u1 : u3), ua[m]);
-      }
-#pragma unroll
-      for (int n = 0; n < NTILES; n += 2) {
-        uint32_t kb[SP][4];
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t va[SP][4];
 #pragma unroll
         for (int p = 0; p < SP; ++p)
-          ldsm4t(kb[p], &sm.k[p][16 * kk + (lane & 7) + ((lane >> 3) & 1) * 8][8 * n + ((lane >> 4) & 1) * 8]);
+          ldsm4t(va[p], &sm.v[p][16 * kk + (lane & 7) + ((lane >> 4) & 1) * 8][16 * warp + ((lane >> 3) & 1) * 8]);
+        const float u0 = sm.upd[16 * kk + gc], u1 = sm.upd[16 * kk + gc + 1];
+        const float u2 = sm.upd[16 * kk + gc + 8], u3 = sm.upd[16 * kk + gc + 9];
+        uint32_t ua[4][3];
 #pragma unroll
-        for (int i = 2; i >= 0; --i) {
-          const uint32_t af[4] = {ua[0][i], ua[1][i], ua[2][i], ua[3][i]};
+        for (int m = 0; m < 4; ++m) {
+          float x = 0.f, y = 0.f;
 #pragma unroll
-          for (int j = SP - 1; j >= 0; --j) {
-            if (i + j > 2) continue;
-            mma(add[n], af, kb[j][0], kb[j][1]);
-            mma(add[n + 1], af, kb[j][2], kb[j][3]);
+          for (int p = SP - 1; p >= 0; --p) x += sm100::bf16_lo(va[p][m]), y += sm100::bf16_hi(va[p][m]);
+          split2<3>(x * (m < 2 ? u0 : u2), y * (m < 2 ? u1 : u3), ua[m]);
+        }
+#pragma unroll
+        for (int n = 0; n < kPart; n += 2) {
+          if (8 * (part + n) >= a.NK) continue;
+          uint32_t kb[SP][4];
+#pragma unroll
+          for (int p = 0; p < SP; ++p)
+            ldsm4t(kb[p],
+                   &sm.k[p][16 * kk + (lane & 7) + ((lane >> 3) & 1) * 8][8 * (part + n) + ((lane >> 4) & 1) * 8]);
+#pragma unroll
+          for (int i = 2; i >= 0; --i) {
+            const uint32_t af[4] = {ua[0][i], ua[1][i], ua[2][i], ua[3][i]};
+#pragma unroll
+            for (int j = SP - 1; j >= 0; --j) {
+              if (i + j > 2) continue;
+              mma(kLow && i + j ? low[kLow ? n : 0] : add[n], af, kb[j][0], kb[j][1]);
+              mma(kLow && i + j ? low[kLow ? n + 1 : 0] : add[n + 1], af, kb[j][2], kb[j][3]);
+            }
           }
         }
       }
+#pragma unroll
+      for (int n = 0; n < kPart; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (kLow) add[n][e] += low[n][e];
+          st[part + n][e] = fmaf(st[part + n][e], dec, add[n][e]);
+        }
     }
-#pragma unroll
-    for (int n = 0; n < NTILES; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) st[n][e] = fmaf(st[n][e], dec, add[n][e]);
 
     if (a.dump && !a.reverse && (ci == chunks - 1 || ((ci + 1) * kLaChunk) % a.window == 0)) {
       const int64_t w = un.window + ((int64_t)ci * kLaChunk) / a.window;

@@ -12,6 +12,7 @@ namespace ssd {
 constexpr double kLaLogMin = -150.0;
 constexpr int kLaChunk = 64;   // tokens of a block of the chunked form (general kernel)
 constexpr int kLaSlice = 64;   // rows of the value dimension one CTA takes (general kernel)
+constexpr int kLaMinWindow = 128;  // tokens of the smallest window
 constexpr int kLaMaxDim = 128; // largest query/key and value dimension
 
 // A window: `len` tokens from t0, all of sequence `seq`, the idx-th window of that sequence.

@@ -240,8 +240,8 @@ int la_validate(const ssd_shape* s, const int32_t* cu) {
   if (s->batch > (1 << 30) || s->seqlen > (1 << 30) || (cu && s->nseq > (1 << 24))) return SSD_ERR_UNSUPPORTED;
   const int64_t tokens = s->batch * s->seqlen, rows = cu ? s->nseq : s->batch;
   if (tokens > ((int64_t)1 << 30) || rows > (1 << 24)) return SSD_ERR_UNSUPPORTED;
-  // the largest grid: windows of 128 tokens, two slices a head
-  if ((tokens / 128 + rows + 1) * s->nheads * 2 > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
+  // the largest grid: the smallest windows, two slices a head
+  if ((tokens / kLaMinWindow + rows + 1) * s->nheads * 2 > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
   if (s->cu_seqlens_host && cu) {
     const int32_t* c = s->cu_seqlens_host;
     if (c[0] != 0 || (int64_t)c[s->nseq] != tokens) return SSD_ERR_BAD_SEQLENS;
@@ -270,10 +270,14 @@ struct Plan {
 // and value alone and a scan over the windows give; that pass costs about 0.6 of the full one,
 // and the two launches before it the time of 12 + 4 passes blocks of 64 tokens (30 - 50 us).
 // With k of the sequences of n blocks cut, in blocks' times,
-//   n max(rounds of the others, all the work / resident) + 0.6 n k lanes / resident + 12 + 4 passes
+//   n max(rounds of the others, all the work / resident) + 0.6 n k lanes / resident + launches
 // and the k with the least is taken.  (2048 tokens: of 8 sequences x 40 pairs of heads one is
 // cut, 306 us instead of 330; of 8 x 32 none.)
-Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, int passes, int64_t resident) {
+// The general kernel runs the passes one after another, so `lanes` counts one of them and the
+// passes' number does not matter; its blocks take longer (fp32 with 128 columns: 7 us), so the
+// launches weigh less: `launches` = 5 blocks, 2 for fp32.  (Gradients of 2 fp32 sequences of 777
+// tokens, 8 heads: windows of 128 tokens, FIGURE.)
+Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, double launches, int64_t resident) {
   const int64_t tokens = s->batch * s->seqlen, rows = cu ? s->nseq : s->batch;
   Plan p{};
   p.window = 512;
@@ -283,12 +287,14 @@ Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, int passes,
     // a packed batch may hold one long sequence among short ones: only many sequences fill the
     // GPU whatever their lengths
     if ((double)rows * (double)lanes < 4.0 * resident && tokens > 256) cut = rows;
-  } else if (s->seqlen > 256) {
+  } else if (s->seqlen > kLaMinWindow) {
     const double n = (double)((s->seqlen + kLaChunk - 1) / kLaChunk);
     double best = n * (double)((rows * lanes + resident - 1) / resident);
     for (int64_t k = 1; k <= std::min<int64_t>(rows, 1024); ++k) {
       const double work = (double)(rows * lanes) / resident, whole = (double)(((rows - k) * lanes + resident - 1) / resident);
-      const double time = n * std::max(whole, work) + 0.6 * n * (double)(k * lanes) / resident + 12 + 4 * passes;
+      const double least = (double)(kLaMinWindow / kLaChunk);  // a window's blocks follow one another
+      const double time = std::max(n * std::max(whole, work), least) +
+                          0.6 * std::max(n * (double)(k * lanes) / resident, least) + launches;
       if (time < best) best = time, cut = k;
     }
   }
@@ -296,7 +302,7 @@ Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, int passes,
     p.whole = (int)(rows - cut);
     const int64_t cut_tokens = cu ? tokens : cut * s->seqlen;
     p.window = 1024;
-    while (p.window > 128 && cut_tokens / p.window * lanes < resident) p.window /= 2;
+    while (p.window > kLaMinWindow && cut_tokens / p.window * lanes < resident) p.window /= 2;
   }
   p.dense_windows = (int)std::max<int64_t>(1, (s->seqlen + p.window - 1) / p.window);
   const int64_t most = cu ? tokens / p.window + rows : rows * p.dense_windows;
@@ -310,7 +316,8 @@ bool wants_tc(const ssd_shape* s) {
   return s->io_dtype == SSD_BF16 && s->headdim % 8 == 0 && s->dstate % 8 == 0 && path_setting() != SSD_PATH_SIMT;
 }
 Plan plan_for(const ssd_shape* s, const int32_t* cu, bool tc, int64_t lanes, int passes) {
-  return make_plan(s, cu, lanes, passes, (tc ? 1 : 3) * (int64_t)device_sm_count());
+  const bool f32 = s->io_dtype == SSD_F32;
+  return make_plan(s, cu, lanes, tc ? 12 + 4 * passes : f32 ? 2 : 5, (tc || f32 ? 1 : 3) * (int64_t)device_sm_count());
 }
 
 // Passes over one problem, with the windows' states first where it is segmented: side by side in
