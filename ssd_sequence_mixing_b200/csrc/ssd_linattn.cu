@@ -84,17 +84,18 @@ struct Smem {
   float dots[4][kLaChunk];
 };
 
-// 64 rows (tokens) x `cols` columns of a (tokens, heads, dim) array into planes; rows past
+// 64 rows (tokens) x COLS columns of a (tokens, heads, dim) array into planes; rows past
 // `rows` and columns past dim - c0 become zeros.
-template <int SP, int PITCH>
-__device__ __forceinline__ void load_tile(__nv_bfloat16 (*dst)[kLaChunk][PITCH], int cols, const void* src, int64_t t0,
-                                          int rows, int heads, int head, int dim, int c0) {
-  const int valid = min(cols, dim - c0);
+template <int SP, int COLS, int PITCH>
+__device__ __forceinline__ void load_tile(__nv_bfloat16 (*dst)[kLaChunk][PITCH], const void* src, int64_t t0, int rows,
+                                          int heads, int head, int dim, int c0) {
+  static_assert(COLS * kLaChunk / 4 % (8 * kThreads) == 0, "whole groups of loads");
+  const int valid = min(COLS, dim - c0);
   if constexpr (SP == 1) {
     const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(src) + (t0 * heads + head) * (int64_t)dim + c0;
     const int64_t pitch = (int64_t)heads * dim;
     if (dim % 8 == 0) {  // every row starts on a 16-byte boundary
-      const int vec = cols / 8;
+      constexpr int vec = COLS / 8;
       for (int e = threadIdx.x; e < kLaChunk * vec; e += kThreads) {
         const int r = e / vec, c = (e % vec) * 8;
         const bool in = r < rows && c < valid;
@@ -105,23 +106,57 @@ __device__ __forceinline__ void load_tile(__nv_bfloat16 (*dst)[kLaChunk][PITCH],
                      : "memory");
       }
     } else {
-      for (int e = threadIdx.x; e < kLaChunk * cols; e += kThreads) {
-        const int r = e / cols, c = e % cols;
+      for (int e = threadIdx.x; e < kLaChunk * COLS; e += kThreads) {
+        const int r = e / COLS, c = e % COLS;
         dst[0][r][c] = r < rows && c < valid ? base[r * pitch + c] : __float2bfloat16_rn(0.f);
       }
     }
   } else {
+    // eight loads of a thread in flight (one after another, a block of 64 tokens took 25 us more)
+    constexpr int kFlight = 8;
     const float* base = static_cast<const float*>(src) + (t0 * heads + head) * (int64_t)dim + c0;
     const int64_t pitch = (int64_t)heads * dim;
-    const int pairs = cols / 2;
-    for (int e = threadIdx.x; e < kLaChunk * pairs; e += kThreads) {
-      const int r = e / pairs, c = (e % pairs) * 2;
-      const float x = r < rows && c < valid ? base[r * pitch + c] : 0.f;
-      const float y = r < rows && c + 1 < valid ? base[r * pitch + c + 1] : 0.f;
+    const int padded = min(COLS, (valid + 15) & ~15);  // columns that the products read
+    auto put = [&](int r, int c, float x, float y) {
       uint32_t pl[SP];
       split2<SP>(x, y, pl);
 #pragma unroll
       for (int p = 0; p < SP; ++p) *reinterpret_cast<uint32_t*>(&dst[p][r][c]) = pl[p];
+    };
+    if (dim % 4 == 0) {  // every row starts on a 16-byte boundary
+      constexpr int kVec = COLS / 4;
+      for (int e0 = threadIdx.x; e0 < kLaChunk * kVec; e0 += kFlight * kThreads) {
+        float4 x[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int e = e0 + i * kThreads, r = e / kVec, c = (e % kVec) * 4;
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < rows && c < valid) x[i] = __ldg(reinterpret_cast<const float4*>(base + r * pitch + c));
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int e = e0 + i * kThreads, r = e / kVec, c = (e % kVec) * 4;
+          if (c >= padded) continue;
+          put(r, c, x[i].x, x[i].y);
+          put(r, c + 2, x[i].z, x[i].w);
+        }
+      }
+    } else {
+      constexpr int kPairs = COLS / 2;
+      for (int e0 = threadIdx.x; e0 < kLaChunk * kPairs; e0 += kFlight * kThreads) {
+        float x[kFlight][2];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int e = e0 + i * kThreads, r = e / kPairs, c = (e % kPairs) * 2;
+          x[i][0] = r < rows && c < valid ? __ldg(base + r * pitch + c) : 0.f;
+          x[i][1] = r < rows && c + 1 < valid ? __ldg(base + r * pitch + c + 1) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int e = e0 + i * kThreads, r = e / kPairs, c = (e % kPairs) * 2;
+          if (c < padded) put(r, c, x[i][0], x[i][1]);
+        }
+      }
     }
   }
 }
@@ -136,7 +171,9 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
   constexpr int KS = NT / 16, NTILES = NT / 8;
   // fp32 operands: the products of lower planes have accumulators of their own.  An accumulation
   // in the tensor core truncates to the sum's last bit, and the sum of the highest planes
-  // then takes a sixth of them.
+  // then takes a sixth of them.  Their loops stay rolled where the registers' indices allow:
+  // each instruction runs once a block, and fetching them is what a block of a short window
+  // waits for.
   constexpr bool kLow = SP == 3;
   const int slice = blockIdx.x % slices;
   const int h = (blockIdx.x / slices) % a.H;
@@ -191,9 +228,9 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
         }
     }
     __syncthreads();  // the last block's tiles are no longer read
-    if (!a.states_only) load_tile<SP>(sm.q, NT, a.query, t0, rows, a.q_heads, qh, a.NK, 0);
-    load_tile<SP>(sm.k, NT, a.key, t0, rows, a.k_heads, kh, a.NK, 0);
-    load_tile<SP>(sm.v, kLaSlice, a.value, t0, rows, a.v_heads, vh, a.PV, row0);
+    if (!a.states_only) load_tile<SP, NT>(sm.q, a.query, t0, rows, a.q_heads, qh, a.NK, 0);
+    load_tile<SP, NT>(sm.k, a.key, t0, rows, a.k_heads, kh, a.NK, 0);
+    load_tile<SP, kLaSlice>(sm.v, a.value, t0, rows, a.v_heads, vh, a.PV, row0);
     if constexpr (SP == 1) sm100::cp_async_commit();
     if (hw == 0) {
       // lane l: tokens 2 l and 2 l + 1; tokens past the end do not decay
@@ -251,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
       };
       clear();
       const int n0 = a.reverse ? 2 * warp : 0, n1 = a.reverse ? 8 : 2 * warp + 2;  // column tiles with any j in reach
-#pragma unroll
+#pragma unroll(kLow ? 1 : KS)
       for (int ks = 0; ks < KS; ++ks) {
         if (16 * ks >= a.NK) continue;
         uint32_t qa[SP][4];
@@ -334,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
           acc[n][e] *= sm.row[8 * n + gc + (e & 1)];
           if constexpr (kLow) low[n][e] *= sm.row[8 * n + gc + (e & 1)];
         }
-#pragma unroll
+#pragma unroll(kLow ? 1 : 4)
       for (int kk = 0; kk < 4; ++kk) {
         if (!has_rows) continue;
         uint32_t va[SP][4];
@@ -363,27 +400,31 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
       // acc[n][e]: value row r_lo + 8 (e >> 1), token 8 n + gc + (e & 1)
       if (a.dot) {
         const int64_t dp = (int64_t)a.dot_heads * a.PV;
+        const int64_t dot0 = t0 * dp + (int64_t)(h / a.dot_div) * a.PV;
+        auto dot_at = [&](int i, int r) {  // (outside: any value of the array, unused)
+          const int64_t at = dot0 + (int64_t)min(i, rows - 1) * dp + min(r, a.PV - 1);
+          return SP == 1 ? to_f(static_cast<const __nv_bfloat16*>(a.dot)[at]) : static_cast<const float*>(a.dot)[at];
+        };
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+        for (int n = 0; n < 8; ++n) {
+          float w[2][2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) w[b][x] = dot_at(8 * n + gc + b, r_lo + 8 * x);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const int i = 8 * n + gc + b;
             float s = 0.f;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int r = r_lo + 8 * x;
-              if (i < rows && r < a.PV) {
-                const int64_t at = (t0 + i) * dp + (int64_t)(h / a.dot_div) * a.PV + r;
-                const float w = SP == 1 ? to_f(static_cast<const __nv_bfloat16*>(a.dot)[at])
-                                        : static_cast<const float*>(a.dot)[at];
-                s = fmaf(w, acc[n][2 * x + b], s);
-              }
-            }
+            for (int x = 0; x < 2; ++x)
+              if (i < rows && r_lo + 8 * x < a.PV) s = fmaf(w[b][x], acc[n][2 * x + b], s);
             s += __shfl_xor_sync(0xffffffffu, s, 4);
             s += __shfl_xor_sync(0xffffffffu, s, 8);
             s += __shfl_xor_sync(0xffffffffu, s, 16);
             if (gr == 0) sm.dots[warp][i] = s;
           }
+        }
         __syncthreads();
         for (int i = threadIdx.x; i < rows; i += kThreads)
           a.dots[((int64_t)slice * a.tokens + t0 + i) * a.H + h] =
@@ -438,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, SP == 1 ? 3 : 1) la_general_kernel(L
           add[n][e] = 0.f;
           if constexpr (kLow) low[n][e] = 0.f;
         }
-#pragma unroll
+#pragma unroll(kLow ? 1 : 4)
       for (int kk = 0; kk < 4; ++kk) {
         uint32_t va[SP][4];
 #pragma unroll
