@@ -543,7 +543,9 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
         final_state = torch.empty(states, dtype=torch.float32, device=device)
     _check("final_state", final_state, device, torch.float32, states)
     scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
-    rc = _on_device(_lib.ssd_linear_attention_forward, device, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), scale, _ptr(init_state), _ptr(cu_seqlens), _ptr(y), _ptr(final_state), _handle(stream, device))
+    rc = _on_device(_lib.ssd_linear_attention_forward, device, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
+                    _ptr(log_decay), int(per_token), scale, _ptr(init_state), _ptr(cu_seqlens), _ptr(y),
+                    _ptr(final_state), _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_linear_attention_forward")
     return y, final_state
@@ -571,7 +573,9 @@ def linear_attention_backward(dy: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     dlog = torch.empty_like(log_decay) if need_dlog_decay else None
     dinit = torch.empty(states, dtype=torch.float32, device=device) if init_state is not None else None
     scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
-    rc = _on_device(_lib.ssd_linear_attention_backward, device, ctypes.byref(shape), _ptr(dy), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), scale, _ptr(init_state), _ptr(dfinal_state), _ptr(cu_seqlens), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlog), _ptr(dinit), _handle(stream, device))
+    rc = _on_device(_lib.ssd_linear_attention_backward, device, ctypes.byref(shape), _ptr(dy), _ptr(q), _ptr(k),
+                    _ptr(v), _ptr(log_decay), int(per_token), scale, _ptr(init_state), _ptr(dfinal_state),
+                    _ptr(cu_seqlens), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlog), _ptr(dinit), _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_linear_attention_backward")
     return dq, dk, dv, dlog, dinit
@@ -592,7 +596,8 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
         y = torch.empty_like(v)
     _check("y", y, device, v.dtype, tuple(v.shape))
     scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
-    rc = _on_device(_lib.ssd_linear_attention_step, device, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_row), scale, _ptr(state), _ptr(y), _handle(stream, device))
+    rc = _on_device(_lib.ssd_linear_attention_step, device, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
+                    _ptr(log_decay), int(per_row), scale, _ptr(state), _ptr(y), _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_linear_attention_step")
     return y
@@ -619,7 +624,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     count = beams if count is None else int(count)
     out = torch.empty((batch, count), dtype=torch.float32, device=device)
     tokens, parents = (torch.empty((batch, count), dtype=torch.int32, device=device) for _ in range(2))
-    rc = _on_device(_lib.ssd_beam_select, device, batch, beams, vocab, _io_code(logits.dtype), _ptr(logits), _ptr(scores), _ptr(finished), int(eos), count, _ptr(out), _ptr(tokens), _ptr(parents), _handle(stream, device))
+    rc = _on_device(_lib.ssd_beam_select, device, batch, beams, vocab, _io_code(logits.dtype), _ptr(logits),
+                    _ptr(scores), _ptr(finished), int(eos), count, _ptr(out), _ptr(tokens), _ptr(parents),
+                    _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_beam_select")
     return out, tokens, parents
@@ -648,7 +655,8 @@ def state_reorder(states, parents: torch.Tensor, stream=None) -> None:
     rows = max(1, batch * beams)
     ptrs = (ctypes.c_void_p * max(1, n))(*[s.data_ptr() for s in states])
     sizes = (ctypes.c_int64 * max(1, n))(*[s.numel() // rows * s.element_size() for s in states])
-    rc = _on_device(_lib.ssd_state_reorder, device, batch, beams, _ptr(parents), n, ptrs, sizes, _handle(stream, device))
+    rc = _on_device(_lib.ssd_state_reorder, device, batch, beams, _ptr(parents), n, ptrs, sizes, _handle(stream,
+                    device))
     if rc:
         raise SsdError(rc, "ssd_state_reorder")
 
