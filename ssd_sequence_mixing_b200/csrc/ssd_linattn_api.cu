@@ -240,8 +240,8 @@ int la_validate(const ssd_shape* s, const int32_t* cu) {
   if (s->batch > (1 << 30) || s->seqlen > (1 << 30) || (cu && s->nseq > (1 << 24))) return SSD_ERR_UNSUPPORTED;
   const int64_t tokens = s->batch * s->seqlen, rows = cu ? s->nseq : s->batch;
   if (tokens > ((int64_t)1 << 30) || rows > (1 << 24)) return SSD_ERR_UNSUPPORTED;
-  // the largest grid: the smallest windows, two slices a head
-  if ((tokens / kLaMinWindow + rows + 1) * s->nheads * 2 > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
+  // the longest list of units: the smallest windows, three passes (and room for a step past its end)
+  if ((tokens / kLaMinWindow + rows + 1) * s->nheads * 3 > ((int64_t)1 << 31) - (1 << 16)) return SSD_ERR_UNSUPPORTED;
   if (s->cu_seqlens_host && cu) {
     const int32_t* c = s->cu_seqlens_host;
     if (c[0] != 0 || (int64_t)c[s->nseq] != tokens) return SSD_ERR_BAD_SEQLENS;
