@@ -268,7 +268,7 @@ int ssd_state_prefix(int rank, int64_t nheads, int64_t headdim, int64_t dstate, 
  *   scale       a factor on y (1/sqrt(N) is usual)
  *   init_state, final_state, cu_seqlens  as for ssd_forward, final_state optional
  * Values that are not finite spoil their own sequence and head only, from the start of their
- * block of 128 tokens (in the gradients: also everything before it).
+ * block of 64 tokens (in the gradients: also everything before it).
  * Sums, states and decays are held in 32 bits or more; bf16 outputs are rounded once, after
  * products whose decayed factors are rounded to bf16 once.
  */
@@ -385,8 +385,8 @@ int ssd_profile_dominant(ssd_event_t start, ssd_event_t stop);
 uint64_t ssd_kernel_launch_count(void);
 
 /*
- * Test hooks for the failure path of the tensor-core kernel (process-wide, not
- * thread-safe; meant for tests).  Every device-side wait of that kernel is bounded:
+ * Test hooks for the failure path of the tensor-core kernels (process-wide, not
+ * thread-safe; meant for tests).  Every device-side wait of theirs is bounded:
  * after `wait_limit_cycles` SM clock cycles (0 = the default, 2^32, about 2 s) it gives
  * up, the kernel drains its in-flight copies and tensor-core work, frees tensor memory
  * and returns, and ssd_query_status() reports SSD_ERR_DEVICE_TIMEOUT; the outputs of

@@ -20,6 +20,11 @@
 // the fp32 value to 24 bits, and the products of planes i + j <= 2 are summed, lowest first.
 // With bf16 outputs the masked product P and the state's copy that meets the query are
 // rounded to one plane each (about the output's own rounding); the state itself never is.
+//
+// Measured, fp32: gradients of 2 x 777 tokens, 8 heads, N 96, P 64: 204 us; 256 tokens of 2 heads of
+// 16 x 16: 35 us.  Bound by latency: at 110 to 160 KB of tiles an SM holds one or two CTAs, a
+// scheduler one or two warps, and an instruction takes 5 to 6 cycles (waits for its last one, for
+// instructions and for loads in equal parts), some 5400 of them a warp and block.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

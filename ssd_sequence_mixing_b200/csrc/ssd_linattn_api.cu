@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kGradThreads) la_decay_grad_kernel(LaGrad a) {
 }
 
 // Constant decays: the windows' sums, one block per head.
-__global__ void __launch_bounds__(kGradThreads) la_decay_total_kernel(const double* parts, int windows, const int32_t* count,
-                                                                      int H, float* out) {
+__global__ void __launch_bounds__(kGradThreads)
+    la_decay_total_kernel(const double* parts, int windows, const int32_t* count, int H, float* out) {
   __shared__ double s_warp[kGradThreads / 32];
   const int h = blockIdx.x;
   const int n = count ? *count : windows;
@@ -291,7 +291,8 @@ Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, double laun
     const double n = (double)((s->seqlen + kLaChunk - 1) / kLaChunk);
     double best = n * (double)((rows * lanes + resident - 1) / resident);
     for (int64_t k = 1; k <= std::min<int64_t>(rows, 1024); ++k) {
-      const double work = (double)(rows * lanes) / resident, whole = (double)(((rows - k) * lanes + resident - 1) / resident);
+      const double work = (double)(rows * lanes) / resident;
+      const double whole = (double)(((rows - k) * lanes + resident - 1) / resident);
       const double least = (double)(kLaMinWindow / kLaChunk);  // a window's blocks follow one another
       const double time = std::max(n * std::max(whole, work), least) +
                           0.6 * std::max(n * (double)(k * lanes) / resident, least) + launches;
@@ -411,7 +412,8 @@ extern "C" int ssd_linear_attention_forward(const ssd_shape* s, const void* q, c
   const Plan plan = plan_for(s, cu, tc, tc ? (P <= 64 && hpg % 2 == 0 ? H / 2 : H) : H * la_general_slices(P), 1);
   const TableLayout tl(plan, rows, 0);
   const size_t o_carry = tl.total;
-  const size_t o_dec = o_carry + (plan.segmented(rows) ? up256(sizeof(float) * (size_t)plan.max_windows * H * P * N) : 0);
+  const size_t states = (size_t)plan.max_windows * H * P * N;
+  const size_t o_dec = o_carry + (plan.segmented(rows) ? up256(sizeof(float) * states) : 0);
   const size_t total = o_dec + (plan.segmented(rows) ? up256(sizeof(float) * (size_t)plan.max_windows * H) : 0);
   char* ws = nullptr;
   if (total && scratch_alloc((void**)&ws, total, st) != cudaSuccess) return SSD_ERR_CUDA;
@@ -489,7 +491,10 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
     p.NK = P, p.PV = N;
     p.start = init_state, p.sr = 1, p.sc = N;
     p.out = shared ? (void*)(ws + o_dq) : dq, p.out_f32 = shared;
-    if (decay_grad) p.dump = (float*)(ws + o_send), p.dot = q, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_qdot);
+    if (decay_grad) {
+      p.dump = (float*)(ws + o_send);
+      p.dot = q, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_qdot);
+    }
   }
   {  // dk = pass (v, dy, q), backwards from dfinal^T
     LaPass& p = pass[1];
@@ -499,7 +504,10 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
     p.NK = P, p.PV = N;
     p.start = dfinal_state, p.sr = 1, p.sc = N;
     p.out = shared ? (void*)(ws + o_dk) : dk, p.out_f32 = shared;
-    if (decay_grad) p.dump = (float*)(ws + o_dend), p.dot = k, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_kdot);
+    if (decay_grad) {
+      p.dump = (float*)(ws + o_dend);
+      p.dot = k, p.dot_heads = G, p.dot_div = hpg, p.dots = (float*)(ws + o_kdot);
+    }
   }
   {  // dv = pass (k, q, dy), backwards from dfinal; its last state is dinit
     LaPass& p = pass[2];

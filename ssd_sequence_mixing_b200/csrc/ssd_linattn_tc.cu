@@ -14,23 +14,40 @@
 // dS does not depend on S, so only the last line is a recurrence; everything else of a block
 // runs while the previous one finishes.
 //
-// One CTA per SM takes one head (up to 128 value rows), or two heads of up to 64 rows each
-// that share query and key, and walks the blocks of its unit.  28 warps, each with one task, so
-// that the tasks of several blocks overlap without any of them being interleaved by hand:
-//   load  (1 warp)   query, key, value tiles by TMA, three stages; issues S1
+// One CTA per SM (the shared memory is its own) walks a list of units: a sequence or a window of
+// one, for one head of up to 128 value rows, or for two heads of up to 64 rows each that share
+// query and key.  The list goes through up to three passes (the gradients of query, key and
+// value are the same operator with exchanged operands), so that a batch too small for one pass
+// fills the GPU with three and no CTA waits between them.  28 warps, each with one task, so that
+// the tasks of several blocks and units overlap without any of them being interleaved by hand:
+//   load  (1 warp)   finds the next unit; query, key and value tiles by TMA, three stages
+//                    (two with PL = 3), and the rows that outputs are multiplied with
 //   dS    (1 warp)   issues the products of dS
-//   Y     (1 warp)   issues Yi and Ya (one warp for all products took 110 cycles for each of a
-//                    block's 32 and 10 commits, and was what a block's time was made of)
+//   Y     (1 warp)   issues S1, a block ahead of Yi and Ya (one warp for all products took 110
+//                    cycles for each of a block's 32 and 10 commits, and was what a block's time
+//                    was made of)
 //   gates (1 warp)   the sums of log-decays in 64 bits and the factors from them
 //   mask  (4 warps)  S1 -> P
 //   decay (8 warps)  value -> the planes of upd o value, by transposing loads
 //   state (8 warps)  dS -> S -> the bf16 planes of S
-//   out   (4 warps)  Yi, Ya -> out
+//   out   (4 warps)  Yi, Ya -> out, and the dot products
 // Tensor memory (512 columns): S1 64, Yi 64, Ya 64, dS 128, planes of upd o value 2 x 32, planes
 // of S 2 x 64 (two heads: Ya 128, S 64).
 //
 // With PL = 3 P and S enter their products as three bf16 planes each (fp32 accuracy), which
-// the per-token dot products behind the decay's gradient need.
+// the per-token dot products behind the decay's gradient need; a pass that has none runs in the
+// same instance with one plane.
+//
+// Measured (a block is 64 tokens of a unit, NK = 128): 2.3 us for one head of 128 rows, 2.9 for
+// two of 64, about 5 with three planes.  8 x 2048 tokens, 32 heads, N = P = 128: 187 us, of which
+// HBM needs 87; 80 heads of 64 rows with one query and key: 277 of 57; gradients of 4 x 2048, 16
+// heads: 310 of 36.  Bound by instructions: 12,800 warp instructions a block, of 28 warps that each
+// run their code once a block, issued in 62 % of the cycles; a tenth of the warps' waiting is for
+// instructions (a text of 75 to 95 KB, a seventh of whose fetches miss), while the tensor pipe is
+// active for 27 %.  What changed most on the way: no register spills (a thread's local memory
+// shares the little L1 that 215 KB of shared memory leave: 992 to 460 us for the first case),
+// rolled loops where the text shrinks (460 to 396), and outputs through a staging
+// buffer instead of 2-byte stores (396 to 325 us).
 //
 // Every wait is bounded; one that runs out stops the CTA's roles, which drain what is in
 // flight, and SSD_ERR_DEVICE_TIMEOUT is recorded.
@@ -66,8 +83,8 @@ constexpr uint32_t kDrainPolls = 1u << 22;  // (a drain's bound is not the test 
 
 enum Bar {
   kFull = 0,                     // tiles of a stage have landed
-  kReady = kFull + kMaxStages,   // ... and rows past the sequence's end are zero (decay warps)
-  kFree = kReady + kMaxStages,      // every product that reads the stage is done
+  kReady = kFull + kMaxStages,  // ... and rows past the sequence's end are zero (decay warps)
+  kFree = kReady + kMaxStages,  // every product that reads the stage is done
   kS1Full = kFree + kMaxStages, kS1Free,
   kPFull, kPFree = kPFull + 2,
   kUvFull = kPFree + 2, kUvFree = kUvFull + 2,
@@ -116,7 +133,7 @@ struct TcSmem {
   static constexpr int kBar = kSum + (PL > 1 ? 4 * kSumBytes : 0);
   static constexpr int kFlag = kBar + 8 * kBars;
   static constexpr int kUnits = (kFlag + 4 + 15) / 16 * 16;
-  static constexpr int kBytes = kUnits + kUnitSlots * (int)sizeof(UnitDesc) + 1024;                  // 1024: alignment of the base
+  static constexpr int kBytes = kUnits + kUnitSlots * (int)sizeof(UnitDesc) + 1024;  // 1024: the base's alignment
 };
 
 __device__ __forceinline__ void tmem_ld8(uint32_t t, uint32_t (&r)[8]) {
@@ -148,8 +165,8 @@ __device__ __forceinline__ void tmem_ld_16x256_x1(uint32_t t, uint32_t (&r)[4]) 
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_16x256_x1(uint32_t t, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3])
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
                : "memory");
 }
 __device__ __forceinline__ void tmem_ld_16x256_x2(uint32_t t, uint32_t (&r)[8]) {
@@ -288,9 +305,13 @@ struct Issue {
   __device__ __forceinline__ explicit Issue(const Cta& cta)
       : t(cta), leader(elect_one()), k_major(sdesc_sw128(0, 16, 1024)), mn_major(sdesc_sw128(0, kAtomBytes, 1024)),
         base(smem_u32(cta.smem)) {}
-  __device__ __forceinline__ uint64_t at(uint64_t major, int off) const { return major | (uint64_t)((base + off) >> 4); }
+  __device__ __forceinline__ uint64_t at(uint64_t major, int off) const {
+    return major | (uint64_t)((base + off) >> 4);
+  }
   // K step kk of a K-major tile of 64-column atoms
-  static __device__ __forceinline__ uint64_t koff(int kk) { return (uint64_t)(((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4); }
+  static __device__ __forceinline__ uint64_t koff(int kk) {
+    return (uint64_t)(((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4);
+  }
   // Arrives on the barrier once every product this warp has issued so far is done.
   __device__ __forceinline__ void commit(int bar) const {
     if (leader) umma_commit(&t.bars[bar]);
@@ -706,7 +727,8 @@ __device__ __forceinline__ void decay_role(const Cta& t) {
 #pragma unroll 1
         for (int i = rows + w; i < kC; i += 8)
           if (lane < 8 * kAtoms)
-            *reinterpret_cast<uint4*>(tiles + L::kK + (lane >> 3) * kAtomBytes + i * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(tiles + L::kK + (lane >> 3) * kAtomBytes + i * 128 + (lane & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
         fence_proxy_async();
       }
       t.arrive(kReady + s);
@@ -773,7 +795,8 @@ struct StateAt {
 // in tensor memory (`ds`; no product uses them at that time), in small loops.  Rows are
 // contiguous in memory (sc = 1: 8 rows x 32 bytes an access) or columns are (a lane per row).
 template <int NC, bool STORE>
-__device__ __forceinline__ void move_state(uint32_t ds, const StateAt& at, int lane, int row0, int n0, int rows, int cols) {
+__device__ __forceinline__ void move_state(uint32_t ds, const StateAt& at, int lane, int row0, int n0, int rows,
+                                           int cols) {
   if (at.sc == 1) {
     const int r0 = row0 + (lane >> 2), c0 = n0 + 2 * (lane & 3);
 #pragma unroll 1
@@ -817,8 +840,8 @@ __device__ __forceinline__ void move_state(uint32_t ds, const StateAt& at, int l
   if (!STORE) tmem_st_wait();
 }
 template <int NC>
-__device__ __forceinline__ void put_state(uint32_t ds, const float (&S)[NC], const StateAt& at, int lane, int row0, int n0,
-                                          int rows, int cols) {
+__device__ __forceinline__ void put_state(uint32_t ds, const float (&S)[NC], const StateAt& at, int lane, int row0,
+                                          int n0, int rows, int cols) {
 #pragma unroll
   for (int b = 0; b < NC / 16; ++b) {
     uint32_t v[16];
@@ -964,9 +987,10 @@ __device__ __forceinline__ void state_role(const Cta& t) {
   }
 }
 
-// Yi, Ya -> out: warp q writes rows 32 q .., 16 tokens at a time.  Tensor memory is read in the layout of mma.sync's accumulators (registers are pairs of
-// tokens of one row), turned by transposing stores to shared memory, and written from there
-// in 16-byte pieces (single 2-byte stores took 16 cycles each, 5 of a block's 9 thousand).
+// Yi, Ya -> out: warp q writes rows 32 q .., 16 tokens at a time.  Tensor memory is read in the
+// layout of mma.sync's accumulators (registers are pairs of tokens of one row), turned by
+// transposing stores to shared memory, and written from there in 16-byte pieces (single 2-byte
+// stores took 16 cycles each, 5 of the 9 thousand that a block then had).
 template <int NT, bool PAIR, int PL, bool F32>
 __device__ __forceinline__ void out_role(const Cta& t) {
   using L = TcSmem<NT, PAIR, PL>;
@@ -1028,7 +1052,8 @@ __device__ __forceinline__ void out_role(const Cta& t) {
       if (!out_f32) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const uint8_t* to = stage + (16 * b + 8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf + 16 * ((t.lane >> 3) & 1);
+          const uint8_t* to = stage + (16 * b + 8 * (t.lane >> 4) + (t.lane & 7)) * kOutPitch + 32 * hf +
+                              16 * ((t.lane >> 3) & 1);
           asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(to)),
                        "r"(bf16x2(o[hf][0], o[hf][1])), "r"(bf16x2(o[hf][2], o[hf][3])),
                        "r"(bf16x2(o[hf][4], o[hf][5])), "r"(bf16x2(o[hf][6], o[hf][7]))
@@ -1254,13 +1279,16 @@ cudaError_t launch_la_tc(const LaPass* p, int passes, cudaStream_t st) {
   if (total > (1ll << 31) - 1) return cudaErrorInvalidConfiguration;
   if (total == 0) return cudaSuccess;
   work.total = (int)total;
-  if (exact && f32)
-    return narrow ? launch_one<64, false, kPlanes, true>(maps, work, st) : launch_one<128, false, kPlanes, true>(maps, work, st);
-  if (exact)
-    return narrow ? launch_one<64, false, kPlanes, false>(maps, work, st) : launch_one<128, false, kPlanes, false>(maps, work, st);
-  if (f32) return narrow ? launch_one<64, false, 1, true>(maps, work, st) : launch_one<128, false, 1, true>(maps, work, st);
-  if (pair) return narrow ? launch_one<64, true, 1, false>(maps, work, st) : launch_one<128, true, 1, false>(maps, work, st);
-  return narrow ? launch_one<64, false, 1, false>(maps, work, st) : launch_one<128, false, 1, false>(maps, work, st);
+  if (narrow) {
+    if (exact) return f32 ? launch_one<64, false, kPlanes, true>(maps, work, st)
+                          : launch_one<64, false, kPlanes, false>(maps, work, st);
+    if (f32) return launch_one<64, false, 1, true>(maps, work, st);
+    return pair ? launch_one<64, true, 1, false>(maps, work, st) : launch_one<64, false, 1, false>(maps, work, st);
+  }
+  if (exact) return f32 ? launch_one<128, false, kPlanes, true>(maps, work, st)
+                        : launch_one<128, false, kPlanes, false>(maps, work, st);
+  if (f32) return launch_one<128, false, 1, true>(maps, work, st);
+  return pair ? launch_one<128, true, 1, false>(maps, work, st) : launch_one<128, false, 1, false>(maps, work, st);
 }
 
 }  // namespace ssd
