@@ -263,15 +263,14 @@ __device__ __forceinline__ bool before(const Cand& x, const Cand& y) {
 }
 constexpr Cand kNone{0, 0xFFFFFFFFu, 0};
 
-// Entry e of a list of beam `beam` with the sum `lse`; none where the score is -inf or NaN.
-__device__ __forceinline__ Cand candidate(const Select& a, const uint64_t* keys, int beam, bool first_split, int e,
-                                          double lse, double score, bool finished) {
+// Entry e, with key k, of a list of beam `beam` with the sum `lse`; none where the score is -inf or NaN.
+__device__ __forceinline__ Cand candidate(const Select& a, uint64_t k, int beam, bool first_split, int e, double lse,
+                                          double score, bool finished) {
   if (finished) {
     if (first_split && e == 0 && score > -INFINITY)
       return Cand{ordered((float)score), (uint32_t)beam, key_of(0.f, (uint32_t)a.eos)};
     return kNone;
   }
-  const uint64_t k = keys[e];
   if (!k) return kNone;
   const float v = (float)(score + ((double)key_value(k) - lse));
   if (!(v > -INFINITY)) return kNone;
@@ -292,6 +291,8 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(Select a) {
   const int64_t b = blockIdx.x;
   const int64_t list0 = b * lists;
   if (tid == 0) s_n = 0, s_limit = Cand{1, 0xFFFFFFFFu, 0};
+  // asked for now, needed after the sums (a finished beam's lists were not written: unused)
+  const uint64_t first = tid < lists ? a.keys[(list0 + tid) * a.count] : 0;
   for (int i = warp; i < a.beams; i += kThreads / 32) {  // a warp per beam, a lane or more per split
     if (a.finished && a.finished[b * a.beams + i]) continue;  // (nothing was written for it)
     static_assert(kMaxSplits <= 64, "a lane takes two splits");
@@ -322,17 +323,17 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(Select a) {
   for (int l = tid; l < lists; l += kThreads) {
     const int beam = l / a.splits;
     const bool fin = a.finished && a.finished[b * a.beams + beam];
-    s_head[l] = candidate(a, a.keys + (list0 + l) * a.count, beam, l % a.splits == 0, 0, s_lse[beam],
-                          (double)a.scores[b * a.beams + beam], fin);
+    const uint64_t k = l == tid ? first : a.keys[(list0 + l) * a.count];
+    s_head[l] = candidate(a, k, beam, l % a.splits == 0, 0, s_lse[beam], (double)a.scores[b * a.beams + beam], fin);
   }
   __syncthreads();
-  for (int l0 = 0; l0 < lists; l0 += kThreads) {
-    const int l = l0 + tid;
-    if (l < lists && s_head[l].score) {
-      int r = 0;
-      for (int i = 0; i < lists; ++i) r += before(s_head[i], s_head[l]);
-      if (r == a.count - 1) s_limit = s_head[l];
-    }
+  for (int l = warp; l < lists; l += kThreads / 32) {  // a warp ranks a list
+    const Cand mine = s_head[l];
+    if (!mine.score) continue;
+    int r = 0;
+    for (int i = lane; i < lists; i += 32) r += before(s_head[i], mine);
+    r = __reduce_add_sync(0xffffffffu, r);
+    if (lane == 0 && r == a.count - 1) s_limit = mine;
   }
   __syncthreads();
   const Cand limit = s_limit;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(Select a) {
     if (!s_head[l].score || before(limit, s_head[l])) continue;  // below the limit from the start
     const int beam = l / a.splits;
     const bool fin = a.finished && a.finished[b * a.beams + beam];
-    const Cand c = candidate(a, a.keys + (list0 + l) * a.count, beam, l % a.splits == 0, e, s_lse[beam],
+    const Cand c = candidate(a, a.keys[list0 * a.count + q], beam, l % a.splits == 0, e, s_lse[beam],
                              (double)a.scores[b * a.beams + beam], fin);
     if (c.score && !before(limit, c)) s_cand[atomicAdd(&s_n, 1)] = c;
   }
