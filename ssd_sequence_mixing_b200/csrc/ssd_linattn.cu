@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(1024) la_table_kernel(int64_t tokens, int nseq
   __shared__ int s_bad;
   __shared__ int s_warp[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = t.count[1] = t.count[2] = 0;
   __syncthreads();
   for (int s = tid; s <= nseq; s += blockDim.x) {
     const int v = cu[s];

@@ -38,6 +38,7 @@ struct LaPass {
   const LaWindow* win;         // packed batches: the windows, ...
   const int32_t* first_win;    // ... each sequence's first one (nseq + 1), ...
   const int32_t* win_count;    // ... and their number, or -1 for invalid offsets
+  int32_t* next;               // ... and two counters of units taken (tcgen05 kernel): the full passes', states_only's
   // operands: head h reads head h / div of an array with `heads` heads
   const void *query, *key, *value;
   int q_heads, k_heads, v_heads, q_div, k_div, v_div;
@@ -74,7 +75,7 @@ inline int64_t la_units(const LaPass& p) {
 
 struct LaTable {
   LaWindow* win;
-  int32_t *first_win, *count;
+  int32_t *first_win, *count;  // count: the windows' number, then the two counters of units taken
 };
 
 cudaError_t launch_la_table(int64_t tokens, int nseq, const int32_t* cu, int window, int max_windows, LaTable t,

@@ -303,7 +303,7 @@ Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, double laun
     p.whole = (int)(rows - cut);
     const int64_t cut_tokens = cu ? tokens : cut * s->seqlen;
     p.window = 1024;
-    while (p.window > kLaMinWindow && cut_tokens / p.window * lanes < resident) p.window /= 2;
+    while (p.window > kLaMinWindow && cut_tokens / p.window * lanes < (cu ? 4 : 1) * resident) p.window /= 2;
   }
   p.dense_windows = (int)std::max<int64_t>(1, (s->seqlen + p.window - 1) / p.window);
   const int64_t most = cu ? tokens / p.window + rows : rows * p.dense_windows;
@@ -374,6 +374,7 @@ void set_common(LaPass& p, const ssd_shape* s, const Plan& plan, const int32_t* 
     p.win = (const LaWindow*)(ws + t.win);
     p.first_win = (const int32_t*)(ws + t.first);
     p.win_count = (const int32_t*)(ws + t.count);
+    p.next = (int32_t*)(ws + t.count) + 1;
   }
   p.log_decay = log_decay;
   p.per_token = per_token;

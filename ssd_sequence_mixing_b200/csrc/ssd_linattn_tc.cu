@@ -240,6 +240,7 @@ struct TcWork {
   int first[6];
   int exact[3];        // the pass wants P and S in three planes
   int8_t map[3][4];    // tensor maps of its query, key, value and dot
+  int32_t* next;       // the next unit that no CTA has taken, or null: CTA b takes b, b + grid, ...
   LaPass pass[3];
 };
 struct TcMaps {
@@ -331,8 +332,14 @@ __device__ __forceinline__ void load_role(const Cta& t, const TcWork& work, cons
   int s = 0, use = 0, dot = 0;  // stage, and its use; loads of rows for dot products
   bool ok = true, left = true;
 #pragma unroll 1
-  for (int n = 0, w = (int)blockIdx.x; ok && left; w += (int)gridDim.x) {
+  for (int n = 0, w = (int)blockIdx.x - (int)gridDim.x; ok && left;) {
     // the next unit that has work
+    if (work.next) {
+      if (t.lane == 0) w = atomicAdd(work.next, 1);
+      w = __shfl_sync(0xffffffffu, w, 0);
+    } else {
+      w += (int)gridDim.x;
+    }
     left = w < work.total;
     int part = 0;
 #pragma unroll 1
@@ -1127,8 +1134,7 @@ __device__ __forceinline__ void out_role(const Cta& t) {
   }
 }
 
-// Grid: a CTA per SM at most; CTA b takes units b, b + grid, ... of the list (units of a pass times
-// heads or pairs of heads, heads fastest).
+// Grid: a CTA per SM at most.  The list: units of a pass times heads or pairs of heads, heads fastest.
 template <int NT, bool PAIR, int PL, bool F32>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     la_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcWork work, unsigned int* status,
@@ -1279,6 +1285,9 @@ cudaError_t launch_la_tc(const LaPass* p, int passes, cudaStream_t st) {
   if (total > (1ll << 31) - 1) return cudaErrorInvalidConfiguration;
   if (total == 0) return cudaSuccess;
   work.total = (int)total;
+  // A packed batch's windows are of 1 to `window` tokens: whoever is free takes the next (which CTA
+  // works on a unit does not change its result).  A dense batch's units are alike.
+  work.next = p[0].next ? p[0].next + (p[0].states_only ? 1 : 0) : nullptr;
   if (narrow) {
     if (exact) return f32 ? launch_one<64, false, kPlanes, true>(maps, work, st)
                           : launch_one<64, false, kPlanes, false>(maps, work, st);
