@@ -16,9 +16,9 @@
 //      or above K.
 //   2. one block per batch item joins the sums, forms the scores in 64 bits and picks the best
 //      of the rows' sorted lists by the same argument.
-// Bound by the issue of instructions for large batches (64 x 8 fp32 rows of 128,000: 67 us, 3.9
+// Bound by the issue of instructions for large batches (64 x 8 fp32 rows of 128,000: 66 us, 4.0
 // TB/s; 18 instructions an element, issued in 67 % of the cycles) and by the latency of two
-// launches for one batch item (4 bf16 rows of 50,003: 20 us).  What counted on the way there: a
+// launches for one batch item (4 bf16 rows of 50,003: 19 us).  What counted on the way there: a
 // warp instead of a thread over a chosen thread's elements, all of the merge's entries at once
 // (109 to 67 us), and four vectors in flight with ranks by warp and then by block (139 to 109).
 //

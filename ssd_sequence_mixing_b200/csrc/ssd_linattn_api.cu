@@ -302,8 +302,10 @@ Plan make_plan(const ssd_shape* s, const int32_t* cu, int64_t lanes, double laun
   if (cut) {
     p.whole = (int)(rows - cut);
     const int64_t cut_tokens = cu ? tokens : cut * s->seqlen;
+    // enough windows for every CTA; of a packed batch, whose windows are of all lengths, twice that
+    // (16 sequences of 1 to 8192 tokens, 16 heads: windows of 1024 tokens 201 us, of 512 215)
     p.window = 1024;
-    while (p.window > kLaMinWindow && cut_tokens / p.window * lanes < (cu ? 4 : 1) * resident) p.window /= 2;
+    while (p.window > kLaMinWindow && cut_tokens / p.window * lanes < (cu ? 2 : 1) * resident) p.window /= 2;
   }
   p.dense_windows = (int)std::max<int64_t>(1, (s->seqlen + p.window - 1) / p.window);
   const int64_t most = cu ? tokens / p.window + rows : rows * p.dense_windows;
