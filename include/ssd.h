@@ -267,6 +267,8 @@ int ssd_state_prefix(int rank, int64_t nheads, int64_t headdim, int64_t dstate, 
  *               that token is forgotten), and below -103.9 counts as -infinity
  *   scale       a factor on y (1/sqrt(N) is usual)
  *   init_state, final_state, cu_seqlens  as for ssd_forward, final_state optional
+ * y and final_state may share no bytes with an input or one another (SSD_ERR_INVALID_ARG): to
+ * continue a state, alternate two buffers.
  * Values that are not finite spoil their own sequence and head only, from the start of their
  * block of 64 tokens (in the gradients: also everything before it).
  * Sums, states and decays are held in 32 bits or more; bf16 outputs are rounded once, after
@@ -286,7 +288,8 @@ int ssd_linear_attention_forward(const ssd_shape* shape, const void* q, const vo
  *   dlog_decay    log_decay's layout           fp32, or NULL (not computed, which is cheaper);
  *                 constants: summed over all tokens; 0 where the decay is zero
  *   dinit_state   (nseq_or_batch, H, P, N)     fp32, or NULL
- * No output may alias an input.  Results do not depend on scheduling (no atomics).
+ * No output may share bytes with an input or another output (SSD_ERR_INVALID_ARG).  Results do
+ * not depend on scheduling.
  */
 int ssd_linear_attention_backward(const ssd_shape* shape, const void* dy, const void* q, const void* k, const void* v,
                                   const float* log_decay, int decay_per_token, float scale, const float* init_state,
@@ -300,7 +303,7 @@ int ssd_linear_attention_backward(const ssd_shape* shape, const void* dy, const 
  *   q, k        (batch, G, N);  v, y  (batch, H, P)   io_dtype
  *   log_decay   (batch, H) fp32 with decay_per_row != 0, else (H)
  *   state       (batch, H, P, N) fp32
- * No scratch.
+ * y and state may share no bytes with the others or one another (SSD_ERR_INVALID_ARG).  No scratch.
  */
 int ssd_linear_attention_step(const ssd_shape* shape, const void* q, const void* k, const void* v,
                               const float* log_decay, int decay_per_row, float scale, float* state, void* y,
