@@ -323,8 +323,8 @@ int ssd_linear_attention_step(const ssd_shape* shape, const void* q, const void*
  * A score that is -infinity or not a number (a row with a NaN or +infinity logit) is no
  * continuation.  Where fewer than `count` are left, the last entries are score -infinity,
  * token eos (0 if negative) and their own place modulo `beams` as parent.
- * beams and count 1..64, vocab 1..2^20.  Outputs may not alias inputs.  Two kernels; a few
- * words of pool scratch per row.
+ * beams and count 1..64, vocab 1..2^20.  Outputs may share no bytes with an input or one another
+ * (SSD_ERR_INVALID_ARG).  Two kernels; a few words of pool scratch per row.
  */
 int ssd_beam_select(int64_t batch, int64_t beams, int64_t vocab, ssd_dtype logits_dtype, const void* logits,
                     const float* scores, const uint8_t* finished, int32_t eos, int64_t count, float* out_scores,
@@ -339,7 +339,7 @@ int ssd_beam_select(int64_t batch, int64_t beams, int64_t vocab, ssd_dtype logit
  *              word (SSD_ERR_BAD_PARENT)
  *   buffers    HOST array of nbuf device pointers, each (batch * beams) contiguous rows ...
  *   row_bytes  HOST array: ... of this many bytes (any, 0 allowed)
- * beams 1..64.  Buffers may not overlap (SSD_ERR_INVALID_ARG).  One kernel for up to 128
+ * beams 1..64.  Buffers may not overlap one another or the parents (SSD_ERR_INVALID_ARG).  One kernel for up to 128
  * buffers of 16-byte rows; no scratch.  Both arrays are read before the call returns.
  */
 int ssd_state_reorder(int64_t batch, int64_t beams, const int32_t* parents, int64_t nbuf, void* const* buffers,

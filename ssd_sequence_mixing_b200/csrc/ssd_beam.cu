@@ -460,6 +460,9 @@ extern "C" int ssd_beam_select(int64_t batch, int64_t beams, int64_t vocab, ssd_
                         (const void*)out_tokens, (const void*)out_parents})
     if (p && ((uintptr_t)p & 15u)) return SSD_ERR_MISALIGNED;
   const int64_t rows = batch * beams;
+  if (!buffers_apart({{out_scores, batch * count * 4}, {out_tokens, batch * count * 4}, {out_parents, batch * count * 4}},
+                     {{logits, rows * vocab * (logits_dtype == SSD_BF16 ? 2 : 4)}, {scores, rows * 4}, {finished, rows}}))
+    return SSD_ERR_INVALID_ARG;
   // Splits of a row: enough blocks to fill the GPU, 2048 elements or more in each, and at
   // most kPerThread elements a thread.
   const int64_t fill = (8 * (int64_t)device_sm_count() + rows - 1) / rows;
@@ -528,6 +531,9 @@ extern "C" int ssd_state_reorder(int64_t batch, int64_t beams, const int32_t* pa
   std::sort(spans.get(), spans.get() + n);
   for (int64_t i = 1; i < n; ++i)
     if (spans[i].first < spans[i - 1].second) return SSD_ERR_INVALID_ARG;  // one buffer would be moved twice
+  for (int64_t i = 0; i < n; ++i)  // ... or the parents moved while others read them
+    if (buffers_meet({parents, batch * beams * 4}, {(void*)spans[i].first, (int64_t)(spans[i].second - spans[i].first)}))
+      return SSD_ERR_INVALID_ARG;
   unsigned int* status = device_status_word();
   if (!status) return SSD_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;

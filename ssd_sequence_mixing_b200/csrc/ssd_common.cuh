@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "ssd.h"
 
 namespace ssd {
@@ -134,5 +136,25 @@ cudaError_t launch_segments_logdecay(const int32_t* cu, int nseg, int64_t max_le
                                      const float* A, float* part, float* lam, cudaStream_t st);
 cudaError_t launch_segments_prefix(int nseq, int k, int64_t H, int64_t PN, const float* states, const float* lam,
                                    const float* init, float* out, float* fin, cudaStream_t st);
+
+// Whether no output shares bytes with an input or another output (for kernels whose parts run in
+// any order, so that what one wrote another might still have to read).
+struct Bytes {
+  const void* p;
+  int64_t n;
+};
+inline bool buffers_meet(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x && y && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+}
+inline bool buffers_apart(std::initializer_list<Bytes> outs, std::initializer_list<Bytes> ins) {
+  for (const Bytes* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Bytes& i : ins)
+      if (buffers_meet(*o, i)) return false;
+    for (const Bytes* r = outs.begin(); r != o; ++r)
+      if (buffers_meet(*o, *r)) return false;
+  }
+  return true;
+}
 
 }  // namespace ssd

@@ -257,26 +257,6 @@ bool la_aligned(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
-// Whether no output shares bytes with an input or another output: windows and heads run in any
-// order, so what one wrote another might still have to read.
-struct Bytes {
-  const void* p;
-  int64_t n;
-};
-bool la_apart(std::initializer_list<Bytes> outs, std::initializer_list<Bytes> ins) {
-  auto meet = [](const Bytes& a, const Bytes& b) {
-    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return x && y && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
-  };
-  for (const Bytes* o = outs.begin(); o != outs.end(); ++o) {
-    for (const Bytes& i : ins)
-      if (meet(*o, i)) return false;
-    for (const Bytes* r = outs.begin(); r != o; ++r)
-      if (meet(*o, *r)) return false;
-  }
-  return true;
-}
-
 // Bytes of the operands.
 struct Sizes {
   int64_t qk, vy, decay, state, cu;
@@ -438,7 +418,7 @@ extern "C" int ssd_linear_attention_forward(const ssd_shape* s, const void* q, c
   if (!la_aligned({q, k, v, log_decay, init_state, cu, y, final_state})) return SSD_ERR_MISALIGNED;
   if (rows == 0) return SSD_OK;
   const Sizes z(s, tokens, rows, decay_per_token, cu);
-  if (!la_apart({{y, z.vy}, {final_state, z.state}},
+  if (!buffers_apart({{y, z.vy}, {final_state, z.state}},
                 {{q, z.qk}, {k, z.qk}, {v, z.vy}, {log_decay, z.decay}, {init_state, z.state}, {cu, z.cu}}))
     return SSD_ERR_INVALID_ARG;
   unsigned int* status = device_status_word();
@@ -491,7 +471,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
     return SSD_OK;
   }
   const Sizes z(s, tokens, rows, decay_per_token, cu);
-  if (!la_apart({{dq, z.qk}, {dk, z.qk}, {dv, z.vy}, {dlog_decay, z.decay}, {dinit_state, z.state}},
+  if (!buffers_apart({{dq, z.qk}, {dk, z.qk}, {dv, z.vy}, {dlog_decay, z.decay}, {dinit_state, z.state}},
                 {{dy, z.vy}, {q, z.qk}, {k, z.qk}, {v, z.vy}, {log_decay, z.decay}, {init_state, z.state},
                  {dfinal_state, z.state}, {cu, z.cu}}))
     return SSD_ERR_INVALID_ARG;
@@ -607,7 +587,7 @@ extern "C" int ssd_linear_attention_step(const ssd_shape* s, const void* q, cons
   if (!q || !k || !v || !log_decay || !state || !y) return SSD_ERR_INVALID_ARG;
   if (!la_aligned({q, k, v, log_decay, state, y})) return SSD_ERR_MISALIGNED;
   const Sizes z(s, s->batch, s->batch, decay_per_row, false);
-  if (!la_apart({{y, z.vy}, {state, z.state}}, {{q, z.qk}, {k, z.qk}, {v, z.vy}, {log_decay, z.decay}}))
+  if (!buffers_apart({{y, z.vy}, {state, z.state}}, {{q, z.qk}, {k, z.qk}, {v, z.vy}, {log_decay, z.decay}}))
     return SSD_ERR_INVALID_ARG;
   LaStep a{};
   a.H = (int)s->nheads, a.P = (int)s->headdim, a.N = (int)s->dstate, a.G = (int)s->ngroups, a.hpg = a.H / a.G;
