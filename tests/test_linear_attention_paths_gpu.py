@@ -187,3 +187,52 @@ def test_calls_that_run_at_the_same_time():
         for g, w in zip(got, want):
             assert all(torch.equal(a, b) for a, b in zip(g, w))
     assert ssd.query_status() == 0
+
+
+def test_packed_batches_at_the_same_time_and_replayed():
+    """Packed batches, whose windows go to whichever CTA is free, on three streams at once and as
+    replayed graphs: the same bits as one call alone."""
+    lens = [[1, 2500, 0, 700, 64, 1200], [3000, 3, 129], [40] * 50]
+    xs = [gpu(make(1, 0, 4, 2, 64, 128, "bf16", lengths=n, seed=50 + i)) for i, n in enumerate(lens)]
+    want = [forward(x) + backward(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(3):
+        got = []
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                got.append(forward(x) + backward(x))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(forward(x) + backward(x))
+        graphs.append(g)
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(o, w))
+    assert ssd.query_status() == 0
+
+
+def test_overlapping_outputs_are_refused_and_two_buffers_taken_in_turn():
+    x = make(1, 700, 2, 1, 64, 64, "bf16", seed=60)
+    d = gpu(x)
+    with pytest.raises(ssd.SsdError):
+        ssd.linear_attention_forward(d["q"], d["k"], d["v"], d["log_decay"], init_state=d["init"], final_state=d["init"])
+    with pytest.raises(ssd.SsdError):
+        ssd.linear_attention_forward(d["q"], d["k"], d["v"], d["log_decay"], init_state=d["init"], y=d["v"])
+    # one sequence in two calls, each in a buffer of its own
+    part = lambda a, b, s: ssd.linear_attention_forward(
+        *(d[n][:, a:b].clone(memory_format=torch.contiguous_format) for n in ("q", "k", "v", "log_decay")), init_state=s)
+    y0, mid = part(0, 384, d["init"])
+    y1, fin = part(384, 700, mid)
+    _, _, _, y_ref, fin_ref = reference(x)
+    close("y", torch.cat([y0, y1], dim=1), y_ref, "bf16")
+    close("final_state", fin, fin_ref, "f32")
