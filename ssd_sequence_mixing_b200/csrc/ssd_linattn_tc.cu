@@ -489,9 +489,12 @@ __device__ __forceinline__ void y_role(const Cta& t, int withhold) {
     }
     if (!ok) break;
     if (left1 > 0) {
+      // A whole block's tiles as they landed.  Where the sequence ends inside the block, its keys
+      // past the end are another's until they are zeroed, and a reverse pass's mask (j >= i)
+      // keeps them: a NaN of theirs would meet the zeroed values in Ya, and 0 * NaN is NaN
+      const int bar = ahead.d->rows(ahead.d->chunks - left1) < kC ? kReady : kFull;
       --left1;
-      // the tiles as they landed: what a last block holds past its end is masked in P
-      if (!(ok = t.wait(kFull + s1, s1use)) || !(ok = t.wait_free(kS1Free, g + 1))) break;
+      if (!(ok = t.wait(bar + s1, s1use)) || !(ok = t.wait_free(kS1Free, g + 1))) break;
       tc_fence_after();
       if (mma.leader) {
         const uint64_t q = mma.at(mma.k_major, s1 * L::kStage + L::kQ), k = mma.at(mma.k_major, s1 * L::kStage + L::kK);
