@@ -420,14 +420,14 @@ __device__ __forceinline__ void load_role(const Cta& t, const TcWork& work, cons
       }
     }
   }
-  // after a failure: what was issued lands before the CTA ends
-  if (!ok)
+  // What was issued lands before the CTA ends, whichever role a wait ran out in (at once in a list
+  // that was worked through).  The last use of stage d that was loaded is `use`, or the one before
 #pragma unroll 1
-    for (int d = 0; d < L::kStages; ++d) {
-      const int n = use - (d >= s);  // the last use of stage d that was loaded
-      if (n >= 0) wait_polls(smem_u32(&t.bars[kFull + d]), (uint32_t)n & 1u, kDrainPolls);
-    }
-  if (PL > 1 && !ok)
+  for (int d = 0; d < L::kStages; ++d) {
+    const int n = use - (d >= s);
+    if (n >= 0) wait_polls(smem_u32(&t.bars[kFull + d]), (uint32_t)n & 1u, kDrainPolls);
+  }
+  if (PL > 1)
 #pragma unroll 1
     for (int d = max(0, dot - 2); d < dot; ++d)
       wait_polls(smem_u32(&t.bars[kDotFull + (d & 1)]), (uint32_t)(d >> 1) & 1u, kDrainPolls);
