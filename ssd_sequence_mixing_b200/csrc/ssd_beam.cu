@@ -46,6 +46,9 @@ constexpr int kThreads = 256;
 constexpr int kMaxBeams = 64;
 constexpr int kMaxSplits = 64;
 constexpr int kPerThread = 128;  // elements of a row a thread takes at most
+// Dynamic shared memory of a block at most.  The kernels' limit is set to this, never to what one
+// call needs: it belongs to the process, and another thread's call may be about to launch
+constexpr int kMaxDynamic = 200 * 1024;
 
 // Whole numbers in the order of the values (-0 and 0 equal; 0 is below every value but NaNs).
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -483,7 +486,7 @@ extern "C" int ssd_beam_select(int64_t batch, int64_t beams, int64_t vocab, ssd_
   const size_t list_bytes = sizeof(uint64_t) * (size_t)count * per_vec * (size_t)((vecs + kThreads - 1) / kThreads);
   const size_t cands = (size_t)beams * splits + (size_t)count * count;
   const size_t merge_bytes = sizeof(double) * kMaxBeams + sizeof(Cand) * cands;
-  if (list_bytes > 200 * 1024 || merge_bytes > 200 * 1024) return SSD_ERR_UNSUPPORTED;
+  if (list_bytes > kMaxDynamic || merge_bytes > kMaxDynamic) return SSD_ERR_UNSUPPORTED;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   const size_t n = (size_t)(rows * splits);
   const size_t o_sum = up(n * sizeof(float)), o_keys = o_sum + up(n * sizeof(double)),
@@ -495,9 +498,9 @@ extern "C" int ssd_beam_select(int64_t batch, int64_t beams, int64_t vocab, ssd_
   auto* rows_fn = logits_dtype == SSD_BF16 ? beam_rows_kernel<__nv_bfloat16> : beam_rows_kernel<float>;
   cudaError_t e = cudaSuccess;
   if (list_bytes > 40 * 1024)
-    e = cudaFuncSetAttribute(rows_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)list_bytes);
+    e = cudaFuncSetAttribute(rows_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
   if (e == cudaSuccess && merge_bytes > 40 * 1024)
-    e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_bytes);
+    e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic);
   if (e == cudaSuccess) {
     rows_fn<<<(unsigned)n, kThreads, list_bytes, st>>>(a);
     beam_merge_kernel<<<(unsigned)batch, kThreads, merge_bytes, st>>>(a);
