@@ -423,6 +423,8 @@ __global__ void __launch_bounds__(kReorderThreads) state_reorder_kernel(const __
     if (k < a.beams && s_src[k] != k) base[k * row] = v[k];
 }
 
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 31) - 1;  // of a launch; one buffer's are 2^30 + 2^24 at most
+
 template <typename V>
 cudaError_t launch_reorder(Reorder& a, cudaStream_t st) {
   int64_t blocks = 0;
@@ -432,8 +434,6 @@ cudaError_t launch_reorder(Reorder& a, cudaStream_t st) {
     a.buf[i].tiles = (int)((a.buf[i].row + kReorderThreads - 1) / kReorderThreads);
     blocks += a.batch * a.buf[i].tiles;
   }
-  if (blocks > ((int64_t)1 << 31) - 1) return cudaErrorInvalidConfiguration;
-  if (blocks == 0) return cudaSuccess;
   if (a.beams <= 4)
     state_reorder_kernel<V, 4><<<(unsigned)blocks, kReorderThreads, 0, st>>>(a);
   else if (a.beams <= 8)
@@ -545,22 +545,26 @@ extern "C" int ssd_state_reorder(int64_t batch, int64_t beams, const int32_t* pa
   for (int unit : {16, 4, 1}) {
     Reorder a{};
     a.parents = parents, a.status = status, a.beams = (int)beams, a.batch = batch;
-    for (int64_t i = 0; i <= nbuf; ++i) {
-      if (a.nbuf && (i == nbuf || a.nbuf == kMaxBuffers)) {
-        const cudaError_t e = unit == 16 ? launch_reorder<uint4>(a, st)
-                              : unit == 4 ? launch_reorder<uint32_t>(a, st)
-                                          : launch_reorder<uint8_t>(a, st);
-        if (e == cudaErrorInvalidConfiguration) return SSD_ERR_UNSUPPORTED;
-        if (e != cudaSuccess) return SSD_ERR_CUDA;
-        a.nbuf = 0;
-      }
-      if (i == nbuf || row_bytes[i] == 0) continue;
+    int64_t blocks = 0;
+    auto flush = [&]() {
+      const cudaError_t e = !a.nbuf      ? cudaSuccess
+                            : unit == 16 ? launch_reorder<uint4>(a, st)
+                            : unit == 4  ? launch_reorder<uint32_t>(a, st)
+                                         : launch_reorder<uint8_t>(a, st);
+      a.nbuf = 0, blocks = 0;
+      return e == cudaSuccess;
+    };
+    for (int64_t i = 0; i < nbuf; ++i) {
+      if (row_bytes[i] == 0) continue;
       const int own = row_bytes[i] % 16 == 0 && beams <= 16 ? 16 : row_bytes[i] % 4 == 0 ? 4 : 1;
       if (own != unit) continue;
+      const int64_t mine = batch * ((row_bytes[i] / unit + kReorderThreads - 1) / kReorderThreads);
+      if ((a.nbuf == kMaxBuffers || blocks + mine > kMaxBlocks) && !flush()) return SSD_ERR_CUDA;
       a.buf[a.nbuf].base = buffers[i];
       a.buf[a.nbuf].row = row_bytes[i];
-      ++a.nbuf;
+      ++a.nbuf, blocks += mine;
     }
+    if (!flush()) return SSD_ERR_CUDA;
   }
   return SSD_OK;
 }
