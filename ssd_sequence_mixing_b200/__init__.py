@@ -479,6 +479,21 @@ def _handle(stream, device):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(stream, shape, dtype, device):
+    """Memory for a result of a call on ``stream``, from that stream's own pool: what torch's current
+    stream has freed may still have its writes to come, which ``stream`` does not wait for.  The
+    current stream may go on to read the result, so the memory is not given out again before
+    what it has queued when the result is dropped."""
+    if stream is None or _handle(stream, device) == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)  # (empty_like is 1 us less of host time, where it will do)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_handle(stream, device), device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def _on_device(call, device, *args):
     """The library's call with ``device`` current (the usual case needs no switch)."""
     if torch.cuda.current_device() == device.index:
@@ -537,10 +552,10 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     device, states = v.device, (rows, shape.nheads, shape.headdim, shape.dstate)
     _check("init_state", init_state, device, torch.float32, states)
     if y is None:
-        y = torch.empty_like(v)
+        y = torch.empty_like(v) if stream is None else _empty(stream, v.shape, v.dtype, device)
     _check("y", y, device, v.dtype, tuple(v.shape))
     if final_state is None and return_final:
-        final_state = torch.empty(states, dtype=torch.float32, device=device)
+        final_state = _empty(stream, states, torch.float32, device)
     _check("final_state", final_state, device, torch.float32, states)
     scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
     rc = _on_device(_lib.ssd_linear_attention_forward, device, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
@@ -569,9 +584,9 @@ def linear_attention_backward(dy: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     _check("dy", dy, device, v.dtype, tuple(v.shape))
     _check("init_state", init_state, device, torch.float32, states)
     _check("dfinal_state", dfinal_state, device, torch.float32, states)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dlog = torch.empty_like(log_decay) if need_dlog_decay else None
-    dinit = torch.empty(states, dtype=torch.float32, device=device) if init_state is not None else None
+    dq, dk, dv = (_empty(stream, x.shape, x.dtype, device) for x in (q, k, v))
+    dlog = _empty(stream, log_decay.shape, torch.float32, device) if need_dlog_decay else None
+    dinit = _empty(stream, states, torch.float32, device) if init_state is not None else None
     scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
     rc = _on_device(_lib.ssd_linear_attention_backward, device, ctypes.byref(shape), _ptr(dy), _ptr(q), _ptr(k),
                     _ptr(v), _ptr(log_decay), int(per_token), scale, _ptr(init_state), _ptr(dfinal_state),
@@ -593,7 +608,7 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
     device = v.device
     _check("state", state, device, torch.float32, (rows, shape.nheads, shape.headdim, shape.dstate))
     if y is None:
-        y = torch.empty_like(v)
+        y = torch.empty_like(v) if stream is None else _empty(stream, v.shape, v.dtype, device)
     _check("y", y, device, v.dtype, tuple(v.shape))
     scale = float(shape.dstate) ** -0.5 if scale is None else float(scale)
     rc = _on_device(_lib.ssd_linear_attention_step, device, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
@@ -622,8 +637,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     _check("scores", scores, device, torch.float32, (batch, beams))
     _check("finished", finished, device, torch.bool, (batch, beams))
     count = beams if count is None else int(count)
-    out = torch.empty((batch, count), dtype=torch.float32, device=device)
-    tokens, parents = (torch.empty((batch, count), dtype=torch.int32, device=device) for _ in range(2))
+    out = _empty(stream, (batch, count), torch.float32, device)
+    tokens, parents = (_empty(stream, (batch, count), torch.int32, device) for _ in range(2))
     rc = _on_device(_lib.ssd_beam_select, device, batch, beams, vocab, _io_code(logits.dtype), _ptr(logits),
                     _ptr(scores), _ptr(finished), int(eos), count, _ptr(out), _ptr(tokens), _ptr(parents),
                     _handle(stream, device))
