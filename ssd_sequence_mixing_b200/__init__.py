@@ -201,7 +201,7 @@ def _check(name, t, device, dtype=None, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _prepare(x, dt, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device):
+def _prepare(x, dt, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device, stream=None):
     batch, T, H, P = x.shape
     G, N = B.shape[2], B.shape[3]
     rows = cu_seqlens.numel() - 1 if cu_seqlens is not None else batch
@@ -213,12 +213,17 @@ def _prepare(x, dt, A, B, C, D, init_state, cu_seqlens, y, final_state, return_f
     _check("D", D, device, torch.float32, (H,))
     _check("init_state", init_state, device, torch.float32, (rows, H, P, N))
     _check("cu_seqlens", cu_seqlens, device, torch.int32)
-    pin = device.type == "cpu" and x.is_pinned()
+
+    def empty(shape, dtype):
+        if device.type == "cpu":
+            return torch.empty(shape, dtype=dtype, pin_memory=x.is_pinned())
+        return _empty(stream, shape, dtype, device)
+
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=device, pin_memory=pin)
+        y = empty(x.shape, x.dtype)
     _check("y", y, device, x.dtype, tuple(x.shape))
     if final_state is None and return_final:
-        final_state = torch.empty((rows, H, P, N), dtype=torch.float32, device=device, pin_memory=pin)
+        final_state = empty((rows, H, P, N), torch.float32)
     _check("final_state", final_state, device, torch.float32, (rows, H, P, N))
     return y, final_state
 
@@ -238,7 +243,7 @@ def ssd_forward(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Ten
     device = x.device
     if device.type != "cuda":
         raise ValueError("ssd_forward takes CUDA tensors; use ssd_forward_host for host buffers")
-    y, final_state = _prepare(x, dt, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device)
+    y, final_state = _prepare(x, dt, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device, stream)
     shape = make_shape(x, B, cu_seqlens, cu_seqlens_host)
     if stream is None:
         stream = torch.cuda.current_stream(device)
@@ -271,7 +276,7 @@ def ssd_final_state(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch
     _check("init_state", init_state, device, torch.float32, (rows, H, P, N))
     _check("cu_seqlens", cu_seqlens, device, torch.int32)
     if final_state is None:
-        final_state = torch.empty((rows, H, P, N), dtype=torch.float32, device=device)
+        final_state = _empty(stream, (rows, H, P, N), torch.float32, device)
     _check("final_state", final_state, device, torch.float32, (rows, H, P, N))
     shape = make_shape(x, B, cu_seqlens)
     if stream is None:
@@ -302,7 +307,7 @@ def ssd_forward_noalloc(x, dt, A, B, C, D=None, init_state=None, cu_seqlens=None
     device = x.device
     if device.type != "cuda":
         raise ValueError("ssd_forward_noalloc takes CUDA tensors")
-    y, final_state = _prepare(x, dt, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device)
+    y, final_state = _prepare(x, dt, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device, stream)
     shape = make_shape(x, B, cu_seqlens)
     if stream is None:
         stream = torch.cuda.current_stream(device)
@@ -325,7 +330,7 @@ def ssd_forward_dt(x, dt_raw, A, B, C, D=None, init_state=None, cu_seqlens=None,
     device = x.device
     if device.type != "cuda":
         raise ValueError("ssd_forward_dt takes CUDA tensors")
-    y, final_state = _prepare(x, dt_raw, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device)
+    y, final_state = _prepare(x, dt_raw, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device, stream)
     _check("dt_bias", dt_bias, device, torch.float32, (x.shape[2],))
     pro = SsdDtPrologue(None if dt_bias is None else dt_bias.data_ptr(), int(bool(softplus)), float(dt_min),
                         float(dt_max))
@@ -357,7 +362,7 @@ def causal_conv1d_silu(xbc, weight, bias=None, cu_seqlens=None, out: Optional[to
     _check("bias", bias, device, torch.float32, (ch,))
     _check("cu_seqlens", cu_seqlens, device, torch.int32)
     if out is None:
-        out = torch.empty_like(xbc)
+        out = _empty(stream, xbc.shape, xbc.dtype, device)
     _check("out", out, device, xbc.dtype, tuple(xbc.shape))
     nseq = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
     if stream is None:
@@ -382,7 +387,7 @@ def gated_rmsnorm(y, z, weight, eps: float = 1e-5, out: Optional[torch.Tensor] =
     _check("z", z, device, y.dtype, tuple(y.shape))
     _check("weight", weight, device, torch.float32, (dim,))
     if out is None:
-        out = torch.empty_like(y)
+        out = _empty(stream, y.shape, y.dtype, device)
     _check("out", out, device, y.dtype, tuple(y.shape))
     if stream is None:
         stream = torch.cuda.current_stream(device)
@@ -402,7 +407,7 @@ def segment_logdecay(dt, A, stream=None):
     tokens = dt.numel() // H
     _check("dt", dt, device, torch.float32)
     _check("A", A, device, torch.float32, (H,))
-    out = torch.empty(H, dtype=torch.float32, device=device)
+    out = _empty(stream, (H,), torch.float32, device)
     if stream is None:
         stream = torch.cuda.current_stream(device)
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -423,7 +428,7 @@ def state_prefix(rank: int, states, logdecay, init_state=None, stream=None):
     _check("init_state", init_state, device, torch.float32, (H, P, N))
     if states.shape[0] < rank or logdecay.shape[0] < rank or logdecay.shape[1] != H:
         raise ValueError("states and logdecay must cover the preceding segments")
-    out = torch.empty((H, P, N), dtype=torch.float32, device=device)
+    out = _empty(stream, (H, P, N), torch.float32, device)
     if stream is None:
         stream = torch.cuda.current_stream(device)
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -457,7 +462,7 @@ def ssd_decode_step(x, dt, A, B, C, D, state, y: Optional[torch.Tensor] = None, 
     _check("D", D, device, torch.float32, (H,))
     _check("state", state, device, torch.float32, (batch, H, P, N))
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(stream, x.shape, x.dtype, device)
     _check("y", y, device, x.dtype, (batch, H, P))
     shape = SsdShape(batch, 1, H, P, N, G, 0, _io_code(x.dtype), None)
     if stream is None:
@@ -683,7 +688,7 @@ def ssd_forward_host(x, dt, A, B, C, D=None, init_state=None, cu_seqlens=None, c
     device = torch.device("cpu")
     if x.device.type != "cpu":
         raise ValueError("ssd_forward_host takes host tensors")
-    y, final_state = _prepare(x, dt, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device)
+    y, final_state = _prepare(x, dt, A, B, C, D, init_state, cu_seqlens, y, final_state, return_final, device, stream)
     shape = make_shape(x, B, cu_seqlens)
     if stream is None:
         stream = torch.cuda.current_stream()
