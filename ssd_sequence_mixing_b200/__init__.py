@@ -632,7 +632,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     bool or None: such a beam goes on by ``eos`` alone, its score unchanged.  Returns (scores
     (batch, count) fp32 best first, tokens, parents (batch, count) int32); see ``ssd_beam_select``.
     """
-    device = logits.device
+    device, eos = logits.device, int(eos)
+    if not -2 ** 31 <= eos < 2 ** 31:
+        raise ValueError(f"eos {eos} is no token")
     if device.type != "cuda":
         raise ValueError("beam_select takes CUDA tensors")
     if logits.dim() != 3:
@@ -645,7 +647,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     out = _empty(stream, (batch, count), torch.float32, device)
     tokens, parents = (_empty(stream, (batch, count), torch.int32, device) for _ in range(2))
     rc = _on_device(_lib.ssd_beam_select, device, batch, beams, vocab, _io_code(logits.dtype), _ptr(logits),
-                    _ptr(scores), _ptr(finished), int(eos), count, _ptr(out), _ptr(tokens), _ptr(parents),
+                    _ptr(scores), _ptr(finished), eos, count, _ptr(out), _ptr(tokens), _ptr(parents),
                     _handle(stream, device))
     if rc:
         raise SsdError(rc, "ssd_beam_select")
