@@ -2,21 +2,27 @@
 // over beams and vocabulary, and the reordering of the beams' states that follows it.
 //
 // Selection.  With lse_i = log sum_w exp(x[i,w]) of beam i's logits, the continuations' scores
-// are scores[i] + (x[i,w] - lse_i); the best `count` over all (i, w) are wanted, ties to the
-// lowest i * vocab + w.  The logits are read once:
+// are scores[i] + (x[i,w] - lse_i), formed in 64 bits and compared in fp32, as they are returned; the
+// best `count` over all (i, w) are wanted, equal ones by the lower beam, then the larger logit,
+// then the lower token.  The logits are read once:
 //   1. blocks of 256 threads, several to a row of logits.  A thread goes over its elements
 //      once, four vectors of 16 bytes in flight, and keeps their running maximum, its place,
-//      and the running sum of exp(x - R) with R a multiple of 128 near the maximum.  Each term
-//      is a function of x alone (R is the same for all of a usual row) and the sum is held in
-//      64 bits, so equal rows have equal sums however they are cut among threads, and equal
-//      scores tie.  Let K be the count-th best of the threads' maxima: an element among the
+//      and the running sum of exp(x).  A term is a function t(x) of the logit times an exact
+//      power of two, and the sum is held in 64 bits in a unit of a power of two near the
+//      maximum, so rows of the same logits have sums that differ by the order of 64-bit
+//      additions alone, however they are cut among threads: by some 2^-52, which fp32
+//      scores do not show, but for a score that lies that close to the border of two
+//      (terms taken from a reference near each thread's own maximum differed by 1e-8: one
+//      in some hundred equal rows around 64 did not tie).  Logits beyond 2^20 in size are taken from
+//      such references all the same.
+//      Let K be the count-th best of the threads' maxima: an element among the
 //      row's best is at or above K and belongs to one of the `count` threads whose maximum is
 //      (count other threads would otherwise each hold a better one), so those threads alone go
 //      over their elements (some dozens, still in cache) a second time and hand on what is at
 //      or above K.
 //   2. one block per batch item joins the sums, forms the scores in 64 bits and picks the best
 //      of the rows' sorted lists by the same argument.
-// Bound by the issue of instructions for large batches (64 x 8 fp32 rows of 128,000: 66 us, 4.0
+// Bound by the issue of instructions for large batches (64 x 8 fp32 rows of 128,000: 67.6 us, 3.9
 // TB/s; 18 instructions an element, issued in 67 % of the cycles) and by the latency of two
 // launches for one batch item (4 bf16 rows of 50,003: 19 us).  What counted on the way there: a
 // warp instead of a thread over a chosen thread's elements, all of the merge's entries at once
@@ -66,14 +72,37 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 }
 __device__ __forceinline__ uint32_t key_place(uint64_t k) { return ~(uint32_t)k; }
 
+// The unit of a sum of exponentials: e^ref 2^e.  Logits of usual sizes have ref = 0, so that terms are
+// e^x = t 2^n with t a function of x alone, and going from one unit to another is exact.
+constexpr float kUsual = 1048576.f;  // beyond this, x log2(e) has too few bits after the point: x - ref instead
+constexpr int kStepE = 512;          // e goes in such steps: a sum of 2^20 terms stays below 2^(kStepE + 22)
+struct SumUnit {
+  float ref;
+  int e;
+};
+constexpr SumUnit kNoUnit{-INFINITY, 0};  // of no logit above -inf
+__device__ __forceinline__ double log2_ratio(SumUnit a, SumUnit b) {
+  return ((double)a.ref - (double)b.ref) * 1.4426950408889634 + (double)(a.e - b.e);
+}
+__device__ __forceinline__ SumUnit larger(SumUnit a, SumUnit b) { return log2_ratio(a, b) > 0.0 ? a : b; }
+// The largest of a warp's.
+__device__ __forceinline__ SumUnit warp_largest(SumUnit u) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const SumUnit v{__shfl_xor_sync(0xffffffffu, u.ref, o), __shfl_xor_sync(0xffffffffu, u.e, o)};
+    u = larger(v, u);
+  }
+  return u;
+}
+
 struct Select {
   int beams, vocab, count, splits, per_split;  // per_split: elements of a row in one block
   const void* logits;
   const float* scores;
   const uint8_t* finished;
   int eos;
-  // of each row and split: R, the sum of exp(x - R), the best `count` keys
-  float* row_ref;
+  // of each row and split: the sum of exponentials and its unit, the best `count` keys
+  SumUnit* row_unit;
   double* row_sum;
   uint64_t* keys;
   float* out_scores;
@@ -109,16 +138,31 @@ __device__ __forceinline__ void load_vec(const T* logits, int64_t j, int64_t lo,
   }
 }
 
-// exp(d) for d <= 64, 0 from -200 down, NaN for NaN and +infinity.  The product d * log2(e) is
-// taken with the rounding error it leaves, so the relative error is that of 2^x alone.
-__device__ __forceinline__ float exp_term(float d) {
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(-200.f));
-  constexpr float kL = 1.44269502162933349609375f, kLow = 1.92596299112661746887e-8f;
-  const float y = d * kL;
-  const float low = fmaf(d, kLow, fmaf(d, kL, -y));
+__device__ __forceinline__ SumUnit unit_for(float top) {
+  if (!(fabsf(top) <= kUsual)) return SumUnit{128.f * rintf(top * (1.f / 128.f)), 0};
+  return SumUnit{0.f, kStepE * (int)rintf(top * (1.4426950408889634f / kStepE))};
+}
+
+// add_term's constants.
+__device__ __forceinline__ float unit_low(SumUnit u) { return ((float)u.e - 1000.f) * 0.693147180559945f; }
+__device__ __forceinline__ uint32_t unit_bias(SumUnit u) { return (uint32_t)(1023 - u.e) << 20; }
+
+// 2^d, exact for whole d (0 from -1080 down); NaN for NaN.
+__device__ __forceinline__ double pow2(double d) {
+  const double n = floor(d), f = d - n;
+  return ldexp(f == 0.0 ? 1.0 : exp2(f), (int)fmax(n, -1080.0));
+}
+
+// s + e^d in units of 2^e; a term below 2^-1000 of the unit counts as that (a sum is at least 2^-258 of it).  NaN from a NaN or an infinite d on.
+__device__ __forceinline__ double add_term(double s, float d, float low, uint32_t bias) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(low));
+  constexpr float kL = 1.44269502162933349609375f, kLow = 1.92596299112661746887e-8f;  // log2(e)
+  constexpr float kWhole = 12582912.f;  // 1.5 2^23: adding it rounds to whole numbers, kept in the lowest bits
+  const float y = fmaf(d, kL, kWhole);
+  const float f = fmaf(d, kLow, fmaf(d, kL, kWhole - y));  // the rest, to 2^-26
   float t;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(y));
-  return fmaf(t, low * 0.693147180559945f, t);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(f));
+  return fma((double)t, __hiloint2double((int)((__float_as_uint(y) << 20) + bias), 0), s);
 }
 
 // Rank of `mine` among keys[0 .. n): how many are larger.
@@ -136,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
   __shared__ uint64_t s_key[kThreads];
   __shared__ uint64_t s_sorted[kWarps][32];  // each warp's best keys, in order
   __shared__ double s_sum[kWarps];
-  __shared__ float s_max[kWarps];
+  __shared__ SumUnit s_unit[kWarps];
   __shared__ int s_who[kMaxBeams];  // the threads with the best maxima, in order
   __shared__ uint64_t s_limit;
   __shared__ int s_n;
@@ -152,7 +196,10 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
 
   // vectors of the block: [0, vecs), those that lie in the range as a whole: [in0, in1)
   const int vecs = (int)(j1 - j0), in0 = lo % n != 0, in1 = (int)(hi / n - j0);
-  float m = -INFINITY, R = -INFINITY;
+  float m = -INFINITY;
+  SumUnit unit{0.f, 0};
+  float low = unit_low(unit);
+  uint32_t bias = unit_bias(unit);
   double s = 0.0;
   int from = 0;  // the group of vectors that holds the maximum first
   for (int u = tid; u < vecs; u += kVecs * kThreads) {
@@ -170,19 +217,22 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
 #pragma unroll
       for (int i = 0; i < n; ++i) top = fmaxf(top, x[v][i]);
     if (top > m) {
+      const bool none = m == -INFINITY;
       m = top;
       from = u;
-      if (top - R > 64.f) {  // the first value, or a far larger one
-        const float to = 128.f * rintf(top * (1.f / 128.f));
-        s *= exp((double)R - (double)to);
-        R = to;
+      // the first value, one far above the unit, or a usual one after logits like -1e9
+      if (none || (top - unit.ref) * 1.4426950408889634f - (float)unit.e > (float)kStepE ||
+          (unit.ref < 0.f && top >= -kUsual)) {
+        const SumUnit to = unit_for(top);
+        s *= none ? 0.0 : pow2(log2_ratio(unit, to));  // (0: what -inf counted so far; a NaN stays)
+        unit = to;
+        low = unit_low(to), bias = unit_bias(to);
       }
     }
-    const float ref = R == -INFINITY ? 0.f : R;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
-      for (int i = 0; i < n; ++i) s += (double)exp_term(x[v][i] - ref);  // NaN from an infinite or NaN logit on
+      for (int i = 0; i < n; ++i) s = add_term(s, x[v][i] - unit.ref, low, bias);
   }
   int best = -1;  // place of the maximum in the row
   if (m > -INFINITY) {  // looked up once: at every new maximum it cost a quarter of the loop
@@ -197,10 +247,9 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
   }
   // a thread without an element above -inf has no key
   const uint64_t mine = best >= 0 ? key_of(m, (uint32_t)best) : 0;
-  float bm = R;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-  if (lane == 0) s_max[warp] = bm;
+  if (m == -INFINITY) unit = kNoUnit, s *= 0.0;  // (a NaN stays)
+  SumUnit bm = warp_largest(unit);
+  if (lane == 0) s_unit[warp] = bm;
   s_key[tid] = mine;
   s_sorted[warp][lane] = 0;
   if (tid < kMaxBeams) s_who[tid] = -1;
@@ -210,8 +259,8 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
   if (mine) s_sorted[warp][r] = mine;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) bm = fmaxf(bm, s_max[w]);
-  double sum = s == 0.0 ? 0.0 : s * exp((double)R - (double)bm);
+  for (int w = 0; w < kWarps; ++w) bm = larger(s_unit[w], bm);
+  double sum = s == 0.0 ? 0.0 : s * pow2(log2_ratio(unit, bm));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
@@ -250,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(Select a) {
     double t = 0.0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) t += s_sum[w];
-    a.row_ref[blockIdx.x] = bm;
+    a.row_unit[blockIdx.x] = bm;
     a.row_sum[blockIdx.x] = t;
   }
 }
@@ -299,23 +348,31 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(Select a) {
   for (int i = warp; i < a.beams; i += kThreads / 32) {  // a warp per beam, a lane or more per split
     if (a.finished && a.finished[b * a.beams + i]) continue;  // (nothing was written for it)
     static_assert(kMaxSplits <= 64, "a lane takes two splits");
-    float ref[2], m = -INFINITY;
+    SumUnit unit[2];
     double part[2], sum = 0.0;
+    uint32_t top = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int e = lane + 32 * h;
-      ref[h] = e < a.splits ? a.row_ref[list0 + i * a.splits + e] : -INFINITY;
-      part[h] = e < a.splits ? a.row_sum[list0 + i * a.splits + e] : 0.0;
-      m = fmaxf(m, ref[h]);
+      const bool in = e < a.splits;
+      const int64_t l = list0 + i * a.splits + e;
+      unit[h] = in ? a.row_unit[l] : kNoUnit;
+      part[h] = in ? a.row_sum[l] : 0.0;
+      top = max(top, in ? (uint32_t)(a.keys[l * a.count] >> 32) : 0);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const SumUnit all = warp_largest(larger(unit[1], unit[0]));
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (part[h] != 0.0) sum += part[h] * exp((double)ref[h] - (double)m);
+      if (part[h] != 0.0) sum += part[h] * pow2(log2_ratio(unit[h], all));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_lse[i] = (double)m + log(sum);  // a row of -inf alone: -inf + -inf, and no key to use it
+    // The largest term anew in 64 bits, and the logarithm of the sum's ratio to it: what is left of a
+    // row with one likely token is that token's 0, and no score is above its beam's
+    const float x = key_value((uint64_t)__reduce_max_sync(0xffffffffu, top) << 32);
+    const double exact = exp2(((double)x - (double)all.ref) * 1.4426950408889634 - (double)all.e);
+    sum -= add_term(0.0, x - all.ref, unit_low(all), unit_bias(all));
+    if (sum < 0.0) sum = 0.0;  // (by the rounding of references that differ, of logits beyond 2^20; a NaN stays)
+    if (lane == 0) s_lse[i] = (double)x + log1p(sum / exact);  // (NaN for a row of -inf alone, which has no key)
   }
   for (int i = tid; i < a.count; i += kThreads) {  // what stays where there are too few continuations
     a.out_scores[b * a.count + i] = -INFINITY;
@@ -489,12 +546,12 @@ extern "C" int ssd_beam_select(int64_t batch, int64_t beams, int64_t vocab, ssd_
   if (list_bytes > kMaxDynamic || merge_bytes > kMaxDynamic) return SSD_ERR_UNSUPPORTED;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   const size_t n = (size_t)(rows * splits);
-  const size_t o_sum = up(n * sizeof(float)), o_keys = o_sum + up(n * sizeof(double)),
+  const size_t o_sum = up(n * sizeof(SumUnit)), o_keys = o_sum + up(n * sizeof(double)),
                total = o_keys + up(n * (size_t)count * sizeof(uint64_t));
   cudaStream_t st = (cudaStream_t)stream;
   char* ws = nullptr;
   if (scratch_alloc((void**)&ws, total, st) != cudaSuccess) return SSD_ERR_CUDA;
-  a.row_ref = (float*)ws, a.row_sum = (double*)(ws + o_sum), a.keys = (uint64_t*)(ws + o_keys);
+  a.row_unit = (SumUnit*)ws, a.row_sum = (double*)(ws + o_sum), a.keys = (uint64_t*)(ws + o_keys);
   auto* rows_fn = logits_dtype == SSD_BF16 ? beam_rows_kernel<__nv_bfloat16> : beam_rows_kernel<float>;
   cudaError_t e = cudaSuccess;
   if (list_bytes > 40 * 1024)
