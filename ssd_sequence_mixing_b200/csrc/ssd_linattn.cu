@@ -620,8 +620,8 @@ __global__ void __launch_bounds__(1024) la_table_kernel(int64_t tokens, int nseq
       else
         hi = mid - 1;
     }
-    const int idx = w - t.first_win[lo], t0 = cu[lo] + idx * window;
-    t.win[w] = LaWindow{lo, t0, min(window, cu[lo + 1] - t0), idx};
+    const int t0 = cu[lo] + (w - t.first_win[lo]) * window;
+    t.win[w] = LaWindow{lo, t0, min(window, cu[lo + 1] - t0)};
   }
 }
 

@@ -15,9 +15,9 @@ constexpr int kLaSlice = 64;   // rows of the value dimension one CTA takes (gen
 constexpr int kLaMinWindow = 128;  // tokens of the smallest window
 constexpr int kLaMaxDim = 128; // largest query/key and value dimension
 
-// A window: `len` tokens from t0, all of sequence `seq`, the idx-th window of that sequence.
+// A window: `len` tokens from t0, all of sequence `seq`.
 struct LaWindow {
-  int32_t seq, t0, len, idx;
+  int32_t seq, t0, len;
 };
 
 // One pass over every sequence and head h, in the order of the tokens or (reverse) against it:

@@ -31,7 +31,7 @@ namespace {
 // ------------------------------------------------------------------ finishing the gradients
 struct LaGrad {
   int64_t tokens, seqlen;
-  int nseq, H, size;  // size: NK * PV
+  int H, size;  // size: NK * PV
   const int32_t* cu;
   int window, dense_windows;
   const LaWindow* win;
@@ -555,7 +555,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
   }
   if (e == cudaSuccess && decay_grad) {
     LaGrad g{};
-    g.tokens = tokens, g.seqlen = s->seqlen, g.nseq = (int)rows, g.H = H, g.size = P * N;
+    g.tokens = tokens, g.seqlen = s->seqlen, g.H = H, g.size = P * N;
     g.cu = cu, g.window = plan.window, g.dense_windows = plan.dense_windows;
     g.win = base.win, g.win_count = base.win_count;
     g.s_end = (const float*)(ws + o_send), g.d_end = (const float*)(ws + o_dend);

@@ -849,20 +849,6 @@ __device__ __forceinline__ void move_state(uint32_t ds, const StateAt& at, int l
   }
   if (!STORE) tmem_st_wait();
 }
-template <int NC>
-__device__ __forceinline__ void put_state(uint32_t ds, const float (&S)[NC], const StateAt& at, int lane, int row0,
-                                          int n0, int rows, int cols) {
-#pragma unroll
-  for (int b = 0; b < NC / 16; ++b) {
-    uint32_t v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(S[16 * b + i]);
-    tmem_st16(ds + 16 * b, v);
-  }
-  tmem_st_wait();
-  move_state<NC, true>(ds, at, lane, row0, n0, rows, cols);
-}
-
 // S in registers: warp w (of 8) holds rows 32 (w % 4) .. and half of the columns.  Step c = -1 of a
 // unit takes the start state the way the others take dS, from the same columns, so that there
 // is one piece of code for what follows either.
