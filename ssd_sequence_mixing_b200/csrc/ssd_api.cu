@@ -73,9 +73,17 @@ cudaMemPool_t lib_pool() {
   props.allocType = cudaMemAllocationTypePinned;
   props.location.type = cudaMemLocationTypeDevice;
   props.location.id = dev;
-  if (cudaMemPoolCreate(&p, &props) != cudaSuccess) return nullptr;
-  uint64_t keep = UINT64_MAX;
-  cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+  // Creating a pool belongs to no stream, but would end a capture that is under way in this process
+  // (a first call may be a captured one): allowed for this thread meanwhile.
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+  cudaError_t e = cudaMemPoolCreate(&p, &props);
+  if (e == cudaSuccess) {
+    uint64_t keep = UINT64_MAX;
+    cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+  }
+  if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return nullptr;
   cudaMemPool_t expected = nullptr;
   if (!g_pool[dev].compare_exchange_strong(expected, p)) {
     cudaMemPoolDestroy(p);
