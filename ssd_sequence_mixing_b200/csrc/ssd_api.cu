@@ -358,6 +358,16 @@ int forward_impl(const ssd_shape* s, const void* x, const float* dt, const float
   }
   pb.withhold_carry = g_withhold_carry.load();
 
+  // A replayed graph launches with the epoch it was captured with, on the same scratch: there the flags
+  // of the last replay would look published, so they are cleared first.
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (path == SSD_PATH_TC && cudaStreamIsCapturing(st, &capture) == cudaSuccess &&
+      capture == cudaStreamCaptureStatusActive &&
+      cudaMemsetAsync(ws + w.carry_flag, 0, w.tile_w - w.carry_flag, st) != cudaSuccess) {
+    cudaFreeAsync(ws, st);
+    return SSD_ERR_CUDA;
+  }
+
   // The chunk table: the SIMT path's chunk records, or the tensor-core path's tile
   // prefix over packed sequences (a dense batch needs none).
   cudaError_t e = cudaSuccess;
