@@ -271,8 +271,11 @@ int ssd_state_prefix(int rank, int64_t nheads, int64_t headdim, int64_t dstate, 
  * continue a state, alternate two buffers.
  * Values that are not finite spoil their own sequence and head only, from the start of their
  * block of 64 tokens (in the gradients: also everything before it).
- * Sums, states and decays are held in 32 bits or more; bf16 outputs are rounded once, after
- * products whose decayed factors are rounded to bf16 once.
+ * Sums, states and decays are held in 32 bits or more.  With bf16 operands y is rounded to bf16
+ * once, and two factors of it are rounded once each before their products: decay x (q . k) of a
+ * block's pairs of tokens, and the copy of the state that meets q (the state itself is carried,
+ * and final_state computed, to fp32).  y's relative L2 error is 2.3e-3, of which its own rounding
+ * is 1.7e-3.  With fp32 operands nothing is rounded below 24 bits.
  */
 int ssd_linear_attention_forward(const ssd_shape* shape, const void* q, const void* k, const void* v,
                                  const float* log_decay, int decay_per_token, float scale, const float* init_state,
@@ -286,7 +289,10 @@ int ssd_linear_attention_forward(const ssd_shape* shape, const void* q, const vo
  *   dq, dk        (batch, seqlen, G, N)        io_dtype: summed over the heads that share them
  *   dv            (batch, seqlen, H, P)        io_dtype
  *   dlog_decay    log_decay's layout           fp32, or NULL (not computed, which is cheaper);
- *                 constants: summed over all tokens; 0 where the decay is zero
+ *                 constants: summed over all tokens; 0 where the decay is zero.  With bf16
+ *                 operands it is a difference of sums over dq and dk, whose two rounded factors
+ *                 (see above) are then kept to 24 bits; dv's, and without dlog_decay dq's and
+ *                 dk's, are rounded to bf16 as y's are, so dq and dk differ within that rounding
  *   dinit_state   (nseq_or_batch, H, P, N)     fp32, or NULL
  * No output may share bytes with an input or another output (SSD_ERR_INVALID_ARG).  Results do
  * not depend on scheduling.

@@ -548,8 +548,10 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     q, k (batch, T, G, N) and v (batch, T, H, P) fp32/bf16, H % G == 0, N and P up to 128;
     log_decay (batch, T, H) or one constant per head (H,), fp32; scale: 1/sqrt(N) by default;
     init_state (rows, H, P, N) fp32 or None; cu_seqlens (nseq+1,) int32 (packed batch,
-    batch == 1) or None.  Returns (y, final_state).  Asynchronous on ``stream`` (default:
-    torch's current stream).
+    batch == 1) or None.  Returns (y, final_state), which carry no autograd graph: their gradients
+    are ``linear_attention_backward``'s.  With bf16 operands two factors of y are rounded to bf16 before
+    their products; states are fp32 throughout.  Asynchronous on ``stream`` (default: torch's
+    current stream).
     """
     shape, rows, per_token = _attention_shape(q, k, v, log_decay, cu_seqlens, cu_seqlens_host)
     if v.dim() != 4:
@@ -580,7 +582,9 @@ def linear_attention_backward(dy: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     and dfinal_state (rows, H, P, N) fp32 or None (see ``ssd_linear_attention_backward``).
 
     Returns (dq, dk, dv, dlog_decay, dinit_state) in the inputs' types and layouts; dlog_decay
-    is None with need_dlog_decay=False (cheaper), dinit_state is None without init_state.
+    is None with need_dlog_decay=False, dinit_state is None without init_state.  Without the decays'
+    gradient the call is cheaper, and bf16 dq and dk come from factors rounded to bf16 (as y and dv do)
+    instead of 24 bits.
     """
     shape, rows, per_token = _attention_shape(q, k, v, log_decay, cu_seqlens, cu_seqlens_host)
     if v.dim() != 4:

@@ -22,17 +22,18 @@
 //      or above K.
 //   2. one block per batch item joins the sums, forms the scores in 64 bits and picks the best
 //      of the rows' sorted lists by the same argument.
-// Bound by the issue of instructions for large batches (64 x 8 fp32 rows of 128,000: 67.6 us, 3.9
-// TB/s; 18 instructions an element, issued in 67 % of the cycles) and by the latency of two
-// launches for one batch item (4 bf16 rows of 50,003: 19 us).  What counted on the way there: a
+// Bound by the issue of instructions for large batches (64 x 8 fp32 rows of 128,000, a fifth of them
+// finished and not read: 68 us, 3.3 TB/s of what is read; 20 instructions an element, issued in
+// 69 % of the cycles) and by the latency of two
+// launches for one batch item (4 bf16 rows of 50,003: 20 us).  What counted on the way there: a
 // warp instead of a thread over a chosen thread's elements, all of the merge's entries at once
 // (109 to 67 us), and four vectors in flight with ranks by warp and then by block (139 to 109).
 //
 // Reordering.  state[b, i] <- state[b, parents[b, i]] in place: the beams of one batch item
 // exchange rows only among themselves, so a thread that holds the same 16 bytes of all its
 // beams loads what moves, then stores it; nothing needs a second buffer.  Rows that stay are
-// neither read nor written.  Bound by HBM (16 x 4 rows of 8 layers, 1.8 GB moved: 330 us, 0.84 of
-// the measured copy rate).
+// neither read nor written.  Bound by HBM (16 x 4 rows of 8 layers, 1.8 GB moved: 300 to 350 us, 0.78
+// to 0.92 of the measured copy rate, by box).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

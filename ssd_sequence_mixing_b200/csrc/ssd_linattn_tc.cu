@@ -34,20 +34,27 @@
 // Tensor memory (512 columns): S1 64, Yi 64, Ya 64, dS 128, planes of upd o value 2 x 32, planes
 // of S 2 x 64 (two heads: Ya 128, S 64).
 //
-// With PL = 3 P and S enter their products as three bf16 planes each (fp32 accuracy), which
-// the per-token dot products behind the decay's gradient need; a pass that has none runs in the
-// same instance with one plane.
+// With one plane P and the copy of S that meets the query are rounded to bf16: about the output's own
+// rounding each (y's error 2.3e-3 for 1.7e-3), where two planes of each would be a quarter more
+// products and a second pass of the mask's and the state's stores.  With PL = 3 they enter their
+// products as three bf16 planes each (fp32 accuracy), which the per-token dot products behind the
+// decay's gradient need; a pass that has none runs in the same instance with one plane.
 //
 // Measured (a block is 64 tokens of a unit, NK = 128): 2.3 us for one head of 128 rows, 2.9 for
 // two of 64, about 5 with three planes.  8 x 2048 tokens, 32 heads, N = P = 128: 187 us, of which
-// HBM needs 87; 80 heads of 64 rows with one query and key: 277 of 57; gradients of 4 x 2048, 16
-// heads: 310 of 36.  Bound by instructions: 12,800 warp instructions a block, of 28 warps that each
-// run their code once a block, issued in 62 % of the cycles; a tenth of the warps' waiting is for
-// instructions (a text of 75 to 95 KB, a seventh of whose fetches miss), while the tensor pipe is
-// active for 27 %.  What changed most on the way: no register spills (a thread's local memory
-// shares the little L1 that 215 KB of shared memory leave: 992 to 460 us for the first case),
-// rolled loops where the text shrinks (460 to 396), and outputs through a staging
-// buffer instead of 2-byte stores (396 to 325 us).
+// HBM needs 87; 80 heads of 64 rows with one query and key: 278 of 57; gradients of 4 x 2048, 16
+// heads: 310 of 36.  No unit of the SM is full: of the issue slots 62 % are used for one head of 128
+// rows, 54 % for two of 64, 53 % with three planes; of the tensor pipe 27, 24 and 21 %.  A block is
+// 12,800, 13,700 and (the mean of the gradients' passes) 19,100 warp instructions, of 28 warps
+// that run their code once a block and wait for one another: most of the waiting is for tensor
+// memory and barriers (4 to 6 of 11 to 13 cycles a warp spends on an instruction), 1 to 2 of them for
+// instructions (a text of 75 to 95 KB, a seventh to a quarter of whose fetches miss).
+// What changed most on the way: the state in registers and no spills in the block loops (a
+// thread's local memory shares the little L1 that 215 KB of shared memory leave: 992 to 460 us for
+// the first case), rolled loops where the text shrinks (460 to 396), and outputs through a staging
+// buffer instead of 2-byte stores (396 to 325 us).  The two instances of one plane, one head and bf16
+// outputs spill nothing; two heads 88 bytes of a thread, three planes 56, three planes with fp32
+// outputs 108 (NK = 64: a little less), none of which has been timed apart.
 //
 // Every wait is bounded; one that runs out stops the CTA's roles, which drain what is in
 // flight, and SSD_ERR_DEVICE_TIMEOUT is recorded.
