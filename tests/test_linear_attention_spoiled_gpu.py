@@ -72,3 +72,34 @@ def test_a_spoiled_sequence_leaves_the_others_gradients(batch, heads, path):
         assert ssd.query_status() == 0
     finally:
         ssd.set_path(ssd.PATH_AUTO)
+
+
+@pytest.mark.parametrize("path", [ssd.PATH_AUTO, ssd.PATH_SIMT], ids=["tensor_core", "general"])
+@pytest.mark.parametrize("heads", ["own", "shared", "wide"])
+def test_a_spoiled_head_leaves_the_others_gradients(heads, path):
+    """The same for one head of every sequence; what heads share (dq and dk of a group) is spoiled."""
+    H, G, N, P = HEADS[heads]
+    clean = gpu(make(2, 700, H, G, N, P, "bf16", seed=71))
+    own = G == H
+    ssd.set_path(path)
+    try:
+        want = calls(clean)
+        for operand in ("q", "k", "v", "dy", "log_decay", "init", "dfinal"):
+            if operand in ("q", "k") and not own:
+                continue
+            x = dict(clean)
+            x[operand] = clean[operand].clone()
+            if operand in ("init", "dfinal"):
+                x[operand][:, 1] = float("nan")
+            else:
+                x[operand][:, 300:400, 1] = float("nan")
+            for n, t in calls(x).items():
+                if n.startswith(("dq", "dk")) and not own:
+                    continue
+                dim = 1 if "state" in n else 2
+                keep = torch.tensor([h for h in range(H) if h != 1], device="cuda")
+                assert torch.equal(t.index_select(dim, keep), want[n].index_select(dim, keep)), f"{operand}: {n}"
+        torch.cuda.synchronize()
+        assert ssd.query_status() == 0
+    finally:
+        ssd.set_path(ssd.PATH_AUTO)
