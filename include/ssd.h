@@ -289,10 +289,13 @@ int ssd_linear_attention_forward(const ssd_shape* shape, const void* q, const vo
  *   dq, dk        (batch, seqlen, G, N)        io_dtype: summed over the heads that share them
  *   dv            (batch, seqlen, H, P)        io_dtype
  *   dlog_decay    log_decay's layout           fp32, or NULL (not computed, which is cheaper);
- *                 constants: summed over all tokens; 0 where the decay is zero.  With bf16
- *                 operands it is a difference of sums over dq and dk, whose two rounded factors
- *                 (see above) are then kept to 24 bits; dv's, and without dlog_decay dq's and
- *                 dk's, are rounded to bf16 as y's are, so dq and dk differ within that rounding
+ *                 constants: summed over all tokens; 0 where the decay is zero and at
+ *                 a sequence's first token without init_state.  Elsewhere a difference of sums
+ *                 of q . dq and k . dk, right to some 2e-5 of their size (a gradient far below
+ *                 it, of a decay to next to nothing, is not resolved).  With bf16 operands the
+ *                 two rounded factors (see above) of dq and dk are then kept to 24 bits; dv's, and
+ *                 without dlog_decay dq's and dk's, are rounded to bf16 as y's are, so dq and dk
+ *                 differ within that rounding
  *   dinit_state   (nseq_or_batch, H, P, N)     fp32, or NULL
  * No output may share bytes with an input or another output (SSD_ERR_INVALID_ARG).  Results do
  * not depend on scheduling.

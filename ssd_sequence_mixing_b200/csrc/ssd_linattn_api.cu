@@ -41,6 +41,7 @@ struct LaGrad {
   int slices;
   const float* log_decay;
   int per_token;
+  int from_zero;   // sequences start from no state: their first decay has nothing to act on
   float* out;      // (tokens, H), or null:
   double* parts;   // (window, H) sums over the window's tokens
 };
@@ -65,10 +66,12 @@ __global__ void __launch_bounds__(kGradThreads) la_decay_grad_kernel(LaGrad a) {
   const int w = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t t0;
   int len;
+  bool first;  // of its sequence
   if (a.cu) {
     if (w >= *a.win_count) return;  // (and where the offsets were invalid: -1)
-    t0 = a.win[w].t0, len = a.win[w].len;
+    t0 = a.win[w].t0, len = a.win[w].len, first = t0 == a.cu[a.win[w].seq];
   } else {
+    first = w % a.dense_windows == 0;
     t0 = (int64_t)(w / a.dense_windows) * a.seqlen + (int64_t)(w % a.dense_windows) * a.window;
     len = (int)min((int64_t)a.window, a.seqlen - (int64_t)(w % a.dense_windows) * a.window);
   }
@@ -108,7 +111,10 @@ __global__ void __launch_bounds__(kGradThreads) la_decay_grad_kernel(LaGrad a) {
     }
     if (i >= 0) {
       const double l = (double)a.log_decay[a.per_token ? t * a.H + h : h] * 1.4426950408889634;
-      const double g = l <= kLaLogMin ? 0.0 : carry + before + x;  // a decay of zero has no gradient in its log
+      // a decay of zero has no gradient in its log, nor has one of no state (the sums' difference is
+      // rounding there)
+      const bool none = l <= kLaLogMin || (a.from_zero && first && i == 0);
+      const double g = none ? 0.0 : carry + before + x;
       if (a.out) a.out[t * a.H + h] = (float)g;
       total += g;
     }
@@ -564,7 +570,7 @@ extern "C" int ssd_linear_attention_backward(const ssd_shape* s, const void* dy,
     g.s_end = (const float*)(ws + o_send), g.d_end = (const float*)(ws + o_dend);
     g.q_dots = (const float*)(ws + o_qdot), g.k_dots = (const float*)(ws + o_kdot);
     g.slices = dot_slices;
-    g.log_decay = log_decay, g.per_token = decay_per_token;
+    g.log_decay = log_decay, g.per_token = decay_per_token, g.from_zero = !init_state;
     g.out = decay_per_token ? dlog_decay : nullptr;
     g.parts = decay_per_token ? nullptr : (double*)(ws + o_parts);
     la_decay_grad_kernel<<<dim3((unsigned)plan.max_windows, (unsigned)H), kGradThreads, 0, st>>>(g);
