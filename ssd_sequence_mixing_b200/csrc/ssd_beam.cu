@@ -154,7 +154,8 @@ __device__ __forceinline__ double pow2(double d) {
   return ldexp(f == 0.0 ? 1.0 : exp2(f), (int)fmax(n, -1080.0));
 }
 
-// s + e^d in units of 2^e; a term below 2^-1000 of the unit counts as that (a sum is at least 2^-258 of it).  NaN from a NaN or an infinite d on.
+// s + e^d in units of 2^e; a term below 2^-1000 of the unit counts as that (a sum is at least 2^-258
+// of it).  NaN from a NaN or an infinite d on.
 __device__ __forceinline__ double add_term(double s, float d, float low, uint32_t bias) {
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(low));
   constexpr float kL = 1.44269502162933349609375f, kLow = 1.92596299112661746887e-8f;  // log2(e)

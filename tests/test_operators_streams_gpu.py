@@ -69,3 +69,27 @@ def test_results_that_the_current_stream_reads_are_not_reused(which):
     assert len(junk) == len(want)
     for a, b in zip(kept, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("which", ["forward", "backward", "select"])
+def test_a_capture_that_forks_to_another_stream(which):
+    calls, x = attention_calls()
+    want = [t.clone() for t in calls[which](None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = calls[which](side)
+        torch.cuda.current_stream().wait_stream(side)
+        sums = [t.float().sum() for t in got]
+        del got
+        side.wait_stream(torch.cuda.current_stream())
+        got = calls[which](side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(a, b.float().sum()) for a, b in zip(sums, want))
+    assert ssd.query_status() == 0
