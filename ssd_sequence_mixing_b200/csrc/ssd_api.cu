@@ -83,7 +83,10 @@ cudaMemPool_t lib_pool() {
     cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
   }
   if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
-  if (e != cudaSuccess) return nullptr;
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
   cudaMemPool_t expected = nullptr;
   if (!g_pool[dev].compare_exchange_strong(expected, p)) {
     cudaMemPoolDestroy(p);
@@ -95,7 +98,9 @@ cudaMemPool_t lib_pool() {
 cudaError_t pool_alloc(void** ptr, size_t bytes, cudaStream_t st) {
   cudaMemPool_t pool = lib_pool();
   if (!pool) return cudaErrorMemoryAllocation;
-  return cudaMallocFromPoolAsync(ptr, bytes, pool, st);
+  const cudaError_t e = cudaMallocFromPoolAsync(ptr, bytes, pool, st);
+  if (e != cudaSuccess) cudaGetLastError();  // reported by this call: the next one's checks are not to find it
+  return e;
 }
 
 int64_t nstate_rows(const ssd_shape* s, const int32_t* cu) { return cu ? s->nseq : s->batch; }
