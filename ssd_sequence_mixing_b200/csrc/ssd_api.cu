@@ -378,6 +378,7 @@ int forward_impl(const ssd_shape* s, const void* x, const float* dt, const float
   cudaError_t e = cudaSuccess;
   if (path == SSD_PATH_SIMT || cu) e = ssd::launch_chunk_table(pb, st);
   if (e == cudaSuccess) e = path == SSD_PATH_TC ? ssd::launch_tc(pb, st) : ssd::launch_simt(pb, st);
+  if (e != cudaSuccess) cudaGetLastError();  // (as in pool_alloc)
   const cudaError_t e2 = cudaFreeAsync(ws, st);
   return (e != cudaSuccess || e2 != cudaSuccess) ? SSD_ERR_CUDA : SSD_OK;
 }

@@ -1802,8 +1802,7 @@ cudaError_t launch_mode(const Problem& pb, cudaStream_t st) {
   e = cudaLaunchKernelEx(&cfg, ssd_fused_tc_kernel<NS, MODE>, mx, mb, mc, my, mdt, pb);
   if (pb.prof_stop) cudaEventRecord(pb.prof_stop, st);
   count_launches(1);
-  const cudaError_t left = cudaGetLastError();  // (read in any case: the next call is not to find it)
-  if (e == cudaSuccess) e = left;
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess && getenv("SSD_DEBUG"))
     fprintf(stderr, "ssd: fused kernel launch failed: %s (smem %u, threads %d)\n", cudaGetErrorString(e),
             (unsigned)kDynSmem<NS, MODE>, kThreads);
